@@ -363,8 +363,111 @@ NVFP4RS_API nvfp4_status nvfp4_mx_group_cast_graphsafe(const void* x_bf16, int64
 NVFP4RS_API nvfp4_status nvfp4_mx_dequantize(const uint8_t* data, const uint8_t* scale, int64_t rows,
                                  int64_t cols, float* out_f32, cudaStream_t stream);
 
-/* Output type of nvfp4_row_post_scale. */
+/* ------------------------------------------------- products of the casts
+ * The products that the casts are made for (TransformerEngine #2931, sequence
+ * diagram: a GEMM over row-scaled operands; #3324, summary: the row-scaled
+ * backward of the grouped linear layer), on the block-scaled tensor cores.
+ *
+ * One operand: a row-major matrix in NVFP4 with one fp32 factor a row, as a
+ * cast writes it. Its value is (e2m1(code) * e4m3(scale)) * s2[row].
+ *   - rowwise outputs of a cast: row_data / row_scale / row_s2, [rows, K];
+ *   - colwise outputs: col_data / col_scale / col_s2, per group [K, m_g] at
+ *     byte K*o_g/2 (codes), K*o_g/16 (scales) and entry g*K (factors).
+ * Weights of E groups are E stacked matrices, [E*N, K]: the rowwise cast of a
+ * packed [E*N, K] buffer, or the colwise cast of a packed [E*K, N] buffer
+ * with m_splits = {K, ...}, which holds the groups' transposes.
+ *
+ * Arithmetic of every product below: exact products of codes and block
+ * scales, summed in fp32 by the tensor cores (their own order and rounding),
+ * then fl(fl(sum * s2_J) * s2_I) -- J the token side (wgrad: dy), I the weight
+ * side (wgrad: x) -- and one rounding to the output type. The same inputs
+ * give the same bits in every call form and routing. A value whose code
+ * products exceed fp32 is infinite; a NaN scale byte (0x7F) makes the rows
+ * that use it NaN and no others.
+ *
+ * Requirements (else NVFP4_ERR_INVALID_ARG): every width that is a block
+ * dimension of the cast is a multiple of 16 (K, N, F). Else
+ * NVFP4_ERR_UNSUPPORTED: pointers 16-byte aligned (s2: 4), stacked weight
+ * rows < 2^31, and with NVFP4_SCALE_TILED_128X4 an operand whose matrices are
+ * multiples of 128 rows and of 128 columns (so 128-row groups for x).
+ * With row-major (compact) scales groups may have any number of rows, 0 and
+ * 1 included. K % 32 == 0 takes the faster load path. Buffers must not overlap
+ * the output. Rows of an output at or beyond the routed total are not written.
+ */
+typedef struct {
+  const uint8_t* data;  /* device, codes */
+  const uint8_t* scale; /* device, E4M3 block scales */
+  const float* s2;      /* device, one factor a row */
+  int32_t scale_layout; /* nvfp4_scale_layout of scale */
+} nvfp4_matrix;
+
+/* Output type of the products and of nvfp4_row_post_scale. */
 typedef enum { NVFP4_OUT_F32 = 0, NVFP4_OUT_BF16 = 1 } nvfp4_out_dtype;
+
+/*
+ * Grouped product y_g = X_g W_g^T (forward; with W's colwise cast as w and
+ * dy's rowwise cast as x, the gradient of the input).
+ *   x    HOST pointer to the operand [sum_M, K], rows of the groups packed
+ *   w    HOST pointer to the operand [num_groups*N, K]
+ *   y    device [sum_M, N] of y_dtype (nvfp4_out_dtype)
+ * m_splits_host as for nvfp4_group_amax, any group sizes >= 0 (multiples of
+ * 128 when x has tiled scales). K == 0 gives zeros. One launch.
+ */
+NVFP4RS_API nvfp4_status nvfp4_group_gemm(const nvfp4_matrix* x, int64_t sum_M, int64_t K,
+                              const int64_t* m_splits_host, int32_t num_groups, const nvfp4_matrix* w,
+                              int64_t N, void* y, int32_t y_dtype, cudaStream_t stream);
+
+/* nvfp4_group_gemm with the graph-safe routing of nvfp4_group_amax_graphsafe
+ * (tensor_offsets in elements of x, row offset * K; K > 0; status rules as
+ * there, plus NVFP4_ERR_TIMEOUT if a bounded wait gave up). A memset of
+ * status and one launch. */
+NVFP4RS_API nvfp4_status nvfp4_group_gemm_graphsafe(const nvfp4_matrix* x, int64_t capacity_rows, int64_t K,
+                                        const int64_t* first_dims_dev, const int64_t* tensor_offsets_dev,
+                                        int32_t num_groups, const nvfp4_matrix* w, int64_t N, void* y,
+                                        int32_t y_dtype, int32_t* status_dev, cudaStream_t stream);
+
+/*
+ * Grouped weight gradient dW_g = dY_g^T X_g from the colwise casts of dy
+ * [sum_M, N] and x [sum_M, K]. An empty group's gradient is zero.
+ *   dy, x  HOST pointers to the operands: colwise outputs, per group [N, m_g]
+ *          and [K, m_g]; m_g % 16 == 0 (% 128 with tiled scales)
+ *   dw     device [num_groups, N, K] of dw_dtype
+ * One launch.
+ */
+NVFP4RS_API nvfp4_status nvfp4_group_wgrad(const nvfp4_matrix* dy, const nvfp4_matrix* x, int64_t sum_M,
+                               const int64_t* m_splits_host, int32_t num_groups, int64_t N, int64_t K,
+                               void* dw, int32_t dw_dtype, cudaStream_t stream);
+
+/* nvfp4_group_wgrad with graph-safe routing (tensor_offsets in elements of x,
+ * row offset * K). On a routing error dw is not written. */
+NVFP4RS_API nvfp4_status nvfp4_group_wgrad_graphsafe(const nvfp4_matrix* dy, const nvfp4_matrix* x,
+                                         int64_t capacity_rows, const int64_t* first_dims_dev,
+                                         const int64_t* tensor_offsets_dev, int32_t num_groups, int64_t N,
+                                         int64_t K, void* dw, int32_t dw_dtype, int32_t* status_dev,
+                                         cudaStream_t stream);
+
+/*
+ * Gated feed-forward block of grouped experts, forward: both projections, the
+ * activation and the product in one launch.
+ *   p = X_g W_g^T, W_g [2F, K]: rows 0..F-1 the gate, F..2F-1 the up projection
+ *   h[t][f] = silu(p[t][f]) * p[t][F + f],  silu(v) = v / (1 + e^-v)
+ * in fp32 from the unrounded p, rounded once to bf16.
+ *   x        HOST pointer to the operand [sum_M, K]
+ *   w        HOST pointer to the operand [num_groups*2F, K]
+ *   h        device bf16 [sum_M, F]
+ *   gate_up  device bf16 [sum_M, 2F]: p, rounded, for the gradient; or NULL
+ */
+NVFP4RS_API nvfp4_status nvfp4_group_gated_gemm(const nvfp4_matrix* x, int64_t sum_M, int64_t K,
+                                    const int64_t* m_splits_host, int32_t num_groups, const nvfp4_matrix* w,
+                                    int64_t F, void* h_bf16, void* gate_up_bf16, cudaStream_t stream);
+
+/* nvfp4_group_gated_gemm with graph-safe routing (as nvfp4_group_gemm_graphsafe). */
+NVFP4RS_API nvfp4_status nvfp4_group_gated_gemm_graphsafe(const nvfp4_matrix* x, int64_t capacity_rows, int64_t K,
+                                              const int64_t* first_dims_dev,
+                                              const int64_t* tensor_offsets_dev, int32_t num_groups,
+                                              const nvfp4_matrix* w, int64_t F, void* h_bf16,
+                                              void* gate_up_bf16, int32_t* status_dev, cudaStream_t stream);
+
 
 /*
  * Per-row FP32 scaling of a GEMM output (TransformerEngine #2931, sequence

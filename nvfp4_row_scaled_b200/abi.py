@@ -62,6 +62,12 @@ class MxOutputs(ctypes.Structure):
                 ("col_data", ctypes.c_void_p), ("col_scale", ctypes.c_void_p)]
 
 
+class Matrix(ctypes.Structure):
+    """Mirror of ``nvfp4_matrix``."""
+    _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("s2", ctypes.c_void_p),
+                ("scale_layout", ctypes.c_int32)]
+
+
 def lib():
     """Open the library (once). Raises if it has not been built."""
     global _lib
@@ -94,6 +100,16 @@ def lib():
         L.nvfp4_row_post_scale.restype = ctypes.c_int
         L.nvfp4_group_quantize_noalloc.argtypes = [vp, i64, i64, vp, i32, vp, vp,
                                                    ctypes.POINTER(Outputs), vp]
+        mp = ctypes.POINTER(Matrix)
+        L.nvfp4_group_gemm.argtypes = [mp, i64, i64, vp, i32, mp, i64, vp, i32, vp]
+        L.nvfp4_group_gemm_graphsafe.argtypes = [mp, i64, i64, vp, vp, i32, mp, i64, vp, i32, vp, vp]
+        L.nvfp4_group_gated_gemm.argtypes = [mp, i64, i64, vp, i32, mp, i64, vp, vp, vp]
+        L.nvfp4_group_gated_gemm_graphsafe.argtypes = [mp, i64, i64, vp, vp, i32, mp, i64, vp, vp, vp, vp]
+        L.nvfp4_group_wgrad.argtypes = [mp, mp, i64, vp, i32, i64, i64, vp, i32, vp]
+        L.nvfp4_group_wgrad_graphsafe.argtypes = [mp, mp, i64, vp, vp, i32, i64, i64, vp, i32, vp, vp]
+        for f in ("nvfp4_group_gemm", "nvfp4_group_gemm_graphsafe", "nvfp4_group_gated_gemm",
+                  "nvfp4_group_gated_gemm_graphsafe", "nvfp4_group_wgrad", "nvfp4_group_wgrad_graphsafe"):
+            getattr(L, f).restype = ctypes.c_int
         for f in ("nvfp4_group_amax", "nvfp4_group_cast", "nvfp4_group_amax_graphsafe",
                   "nvfp4_group_cast_graphsafe", "nvfp4_dequantize", "nvfp4_group_quantize",
                   "nvfp4_group_quantize_graphsafe", "nvfp4_group_quantize_noalloc"):
@@ -336,6 +352,184 @@ def nvfp4_dequantize(data: torch.Tensor, scale: torch.Tensor, s2: torch.Tensor, 
                                 _dev(s2, torch.float32, "s2"), int(rows), int(cols),
                                 _dev(out, torch.float32, "out"), _stream(stream))
     _check(rc, "nvfp4_dequantize")
+
+
+# --------------------------------------------------- products of the casts
+
+def matrix(data: torch.Tensor, scale: torch.Tensor, s2: torch.Tensor,
+           scale_layout: int = NVFP4_SCALE_COMPACT) -> Dict[str, object]:
+    """An NVFP4 operand of the products: codes, block scales (in
+    ``scale_layout``) and one fp32 factor a row."""
+    return {"data": data, "scale": scale, "s2": s2, "scale_layout": int(scale_layout)}
+
+
+def row_matrix(out: Dict[str, torch.Tensor], scale_layout: int = NVFP4_SCALE_COMPACT) -> Dict[str, object]:
+    """The rowwise outputs of a cast as an operand."""
+    return matrix(out["row_data"], out["row_scale"], out["row_s2"], scale_layout)
+
+
+def col_matrix(out: Dict[str, torch.Tensor], scale_layout: int = NVFP4_SCALE_COMPACT) -> Dict[str, object]:
+    """The colwise outputs of a cast (each group's transpose) as an operand."""
+    return matrix(out["col_data"], out["col_scale"], out["col_s2"], scale_layout)
+
+
+def _matrix(m: Dict[str, object], rows: int, elements: int, name: str) -> Matrix:
+    """``m`` checked to be ``rows`` factors and ``elements`` codes."""
+    for key, n in (("data", elements // 2), ("scale", elements // 16), ("s2", rows)):
+        if m[key].numel() != n:
+            raise ValueError(f"{name}[{key!r}] must have {n} entries, got {m[key].numel()}")
+    o = Matrix()
+    o.data = _dev(m["data"], torch.uint8, f"{name}['data']").value
+    o.scale = _dev(m["scale"], torch.uint8, f"{name}['scale']").value
+    o.s2 = _dev(m["s2"], torch.float32, f"{name}['s2']").value
+    o.scale_layout = int(m.get("scale_layout", NVFP4_SCALE_COMPACT))
+    return o
+
+
+def _same_device(ref: torch.Tensor, *tensors) -> torch.device:
+    """The one CUDA device of all the tensors (None is skipped)."""
+    for t in tensors:
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"tensors are on {ref.device} and {t.device}")
+    if not ref.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    return ref.device
+
+
+def _parts(*ms):
+    return [m[k] for m in ms for k in ("data", "scale", "s2")]
+
+
+def _on(dev: torch.device, stream, what: str, call) -> None:
+    """Run ``call(stream pointer)`` with ``dev`` current, on its current stream
+    unless one is given."""
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    with torch.cuda.device(dev):
+        rc = call(_stream(stream))
+    _check(rc, what)
+
+
+def _out_dtype(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.float32:
+        return NVFP4_OUT_F32
+    if t.dtype == torch.bfloat16:
+        return NVFP4_OUT_BF16
+    raise ValueError(f"{name} must be float32 or bfloat16")
+
+
+def _width(w: Dict[str, object], x: Dict[str, object], rows: int, what: str) -> int:
+    """Contraction width of x [rows, K] against stacked weights w."""
+    ref, n = (x, rows) if rows else (w, w["s2"].numel())
+    total = 2 * ref["data"].numel()
+    if n and total % n:
+        raise ValueError(f"{what}: {total} codes are not {n} equal rows")
+    return total // n if n else 0
+
+
+def nvfp4_group_gemm(x: Dict[str, object], m_splits: Sequence[int], w: Dict[str, object], y: torch.Tensor,
+                     stream=None) -> None:
+    """y [rows, N] (bf16 or fp32) = X_g W_g^T for each group's rows of x [rows, K]
+    and its matrix of w [E*N, K]. Input gradients: x the rowwise cast of dy, w
+    the colwise cast of the weights."""
+    arr, E = _splits(m_splits)
+    rows, N = y.shape
+    K = _width(w, x, rows, "nvfp4_group_gemm")
+    dt = _out_dtype(y, "y")
+    dev = _same_device(y, *_parts(x, w))
+    xm, wm = _matrix(x, rows, rows * K, "x"), _matrix(w, E * N, E * N * K, "w")
+    yp = _dev(y, y.dtype, "y")
+    _on(dev, stream, "nvfp4_group_gemm", lambda s: lib().nvfp4_group_gemm(
+        ctypes.byref(xm), rows, K, arr, E, ctypes.byref(wm), N, yp, dt, s))
+
+
+def nvfp4_group_gemm_graphsafe(x: Dict[str, object], first_dims: Optional[torch.Tensor],
+                               tensor_offsets: Optional[torch.Tensor], w: Dict[str, object], y: torch.Tensor,
+                               status: torch.Tensor, stream=None, num_groups: Optional[int] = None) -> None:
+    E = _groups(first_dims, num_groups)
+    rows, N = y.shape
+    K = _width(w, x, rows, "nvfp4_group_gemm_graphsafe")
+    dt = _out_dtype(y, "y")
+    dev = _same_device(y, first_dims, tensor_offsets, status, *_parts(x, w))
+    xm, wm = _matrix(x, rows, rows * K, "x"), _matrix(w, E * N, E * N * K, "w")
+    fd, to, st, yp = _routing(first_dims, tensor_offsets, status, E) + (_dev(y, y.dtype, "y"),)
+    _on(dev, stream, "nvfp4_group_gemm_graphsafe", lambda s: lib().nvfp4_group_gemm_graphsafe(
+        ctypes.byref(xm), rows, K, fd, to, E, ctypes.byref(wm), N, yp, dt, st, s))
+
+
+def _routing(first_dims, tensor_offsets, status, E: int):
+    if tensor_offsets is not None and tensor_offsets.numel() != E + 1:
+        raise ValueError(f"tensor_offsets must have {E + 1} entries")
+    return (_dev(first_dims, torch.int64, "first_dims"), _dev(tensor_offsets, torch.int64, "tensor_offsets"),
+            _dev(status, torch.int32, "status"))
+
+
+def _gated(x, w, h, gate_up, E):
+    rows, F = h.shape
+    if gate_up is not None and tuple(gate_up.shape) != (rows, 2 * F):
+        raise ValueError("gate_up must be [rows, 2F]")
+    K = _width(w, x, rows, "nvfp4_group_gated_gemm")
+    return (rows, F, K, _matrix(x, rows, rows * K, "x"), _matrix(w, E * 2 * F, E * 2 * F * K, "w"),
+            _dev(h, torch.bfloat16, "h"), _dev(gate_up, torch.bfloat16, "gate_up"))
+
+
+def nvfp4_group_gated_gemm(x: Dict[str, object], m_splits: Sequence[int], w: Dict[str, object], h: torch.Tensor,
+                           gate_up: Optional[torch.Tensor] = None, stream=None) -> None:
+    """h [rows, F] = silu(X_g Wgate_g^T) * (X_g Wup_g^T); w [E*2F, K] holds each
+    group's gate rows, then its up rows. gate_up [rows, 2F], if given, takes the
+    two projections (bf16) for the gradient."""
+    arr, E = _splits(m_splits)
+    dev = _same_device(h, gate_up, *_parts(x, w))
+    rows, F, K, xm, wm, hp, gp = _gated(x, w, h, gate_up, E)
+    _on(dev, stream, "nvfp4_group_gated_gemm", lambda s: lib().nvfp4_group_gated_gemm(
+        ctypes.byref(xm), rows, K, arr, E, ctypes.byref(wm), F, hp, gp, s))
+
+
+def nvfp4_group_gated_gemm_graphsafe(x: Dict[str, object], first_dims: Optional[torch.Tensor],
+                                     tensor_offsets: Optional[torch.Tensor], w: Dict[str, object], h: torch.Tensor,
+                                     status: torch.Tensor, gate_up: Optional[torch.Tensor] = None, stream=None,
+                                     num_groups: Optional[int] = None) -> None:
+    E = _groups(first_dims, num_groups)
+    dev = _same_device(h, gate_up, first_dims, tensor_offsets, status, *_parts(x, w))
+    rows, F, K, xm, wm, hp, gp = _gated(x, w, h, gate_up, E)
+    fd, to, st = _routing(first_dims, tensor_offsets, status, E)
+    _on(dev, stream, "nvfp4_group_gated_gemm_graphsafe", lambda s: lib().nvfp4_group_gated_gemm_graphsafe(
+        ctypes.byref(xm), rows, K, fd, to, E, ctypes.byref(wm), F, hp, gp, st, s))
+
+
+def _wgrad(dy, x, dw, rows):
+    E, N, K = dw.shape
+    return (E, N, K, _matrix(dy, E * N, rows * N, "dy"), _matrix(x, E * K, rows * K, "x"),
+            _dev(dw, dw.dtype, "dw"), _out_dtype(dw, "dw"))
+
+
+def nvfp4_group_wgrad(dy: Dict[str, object], x: Dict[str, object], m_splits: Sequence[int], dw: torch.Tensor,
+                      stream=None) -> None:
+    """dw [E, N, K] (bf16 or fp32) = dY_g^T X_g from the colwise casts of dy
+    [rows, N] and x [rows, K]; zero for an empty group."""
+    arr, E = _splits(m_splits)
+    if dw.shape[0] != E:
+        raise ValueError(f"dw must have {E} matrices")
+    rows = sum(int(m) for m in m_splits)
+    dev = _same_device(dw, *_parts(dy, x))
+    E, N, K, dm, xm, wp, dt = _wgrad(dy, x, dw, rows)
+    _on(dev, stream, "nvfp4_group_wgrad", lambda s: lib().nvfp4_group_wgrad(
+        ctypes.byref(dm), ctypes.byref(xm), rows, arr, E, N, K, wp, dt, s))
+
+
+def nvfp4_group_wgrad_graphsafe(dy: Dict[str, object], x: Dict[str, object], capacity_rows: int,
+                                first_dims: Optional[torch.Tensor], tensor_offsets: Optional[torch.Tensor],
+                                dw: torch.Tensor, status: torch.Tensor, stream=None,
+                                num_groups: Optional[int] = None) -> None:
+    E = _groups(first_dims, num_groups)
+    if dw.shape[0] != E:
+        raise ValueError(f"dw must have {E} matrices")
+    rows = int(capacity_rows)
+    dev = _same_device(dw, first_dims, tensor_offsets, status, *_parts(dy, x))
+    E, N, K, dm, xm, wp, dt = _wgrad(dy, x, dw, rows)
+    fd, to, st = _routing(first_dims, tensor_offsets, status, E)
+    _on(dev, stream, "nvfp4_group_wgrad_graphsafe", lambda s: lib().nvfp4_group_wgrad_graphsafe(
+        ctypes.byref(dm), ctypes.byref(xm), rows, fd, to, E, N, K, wp, dt, st, s))
 
 
 # -------------------------------------------------------- buffer helpers

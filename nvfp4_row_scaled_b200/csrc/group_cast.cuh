@@ -64,6 +64,10 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
                : "memory");
 }
 
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 // Wait for the phase with parity `phase` to complete; false after `tries` tries.
 __device__ __forceinline__ bool mbar_wait_some(uint64_t* bar, uint32_t phase, uint32_t tries) {
   const uint32_t a = smem_addr(bar);

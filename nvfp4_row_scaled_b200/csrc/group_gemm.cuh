@@ -1,0 +1,624 @@
+// group_gemm.cuh -- products of grouped row-scaled NVFP4 matrices on the
+// block-scaled tensor cores.
+//
+// What the casts of this library are made for (TransformerEngine #2931,
+// "Implement per-token NVFP4 fprop recipe", sequence diagram: a GEMM over the
+// row-scaled operands whose output is multiplied back by the row factors;
+// #3324, the row-scaled backward of the grouped linear layer). One kernel
+// body serves
+//   kGemmPlain    y[t][n]  = sx[t] sw[n] sum_k x[t][k] w_g[n][k]      (t in group g)
+//   kGemmGated    h[t][f]  = silu(p[t][f]) * p[t][F + f],  p as above, N = 2F
+//   kGemmWgrad    dw_g[n][k] = sdy[n] sx[k] sum_t dy[t][n] x[t][k]    (t in group g)
+//   kGemmAdapter  kGemmPlain + sum_r u[t][r] b_a[n][r],  a = id[t]
+// where every x, w, dy is e2m1 * e4m3 (a code and the scale of its 16-element
+// block) and s.. the fp32 row factor of the cast.
+//
+// The mathematics on the hardware. A tcgen05.mma of kind mxf4nvf4 multiplies
+// 64 codes of each row, applies both operands' E4M3 scales per 16 codes and
+// accumulates in fp32 in tensor memory; the row factors are constant along
+// the contraction, so they are applied once, in fp32, when the accumulator is
+// read: fl(fl(acc * s_J) * s_I). The result is rounded once to the output type.
+//
+// Orientation. Accumulator LANES (128, the M side of the instruction) are
+// rows of operand I -- weights, or for wgrad the columns of x -- and COLUMNS
+// (N side, any multiple of 16 up to 256) rows of operand J -- tokens, or the
+// columns of dy. The token side is the one whose length varies, from one row
+// to thousands, and the N side is the one that can be cut to 16: a group of
+// one token costs 16 columns, not 128 lanes, while a decode step streams its
+// weights 128 rows at a time. out[J row][I row] is then row-major with the 32
+// lanes of a warp on 32 neighbouring elements.
+//
+// Work split. A persistent CTA per SM walks every gridDim-th tile (128 I rows
+// x `jt` J rows of one group, I tiles innermost so that concurrent CTAs share
+// the token tile and the group's weights in L2). Five roles, joined by
+// mbarriers:
+//   warp 0      data of each 256-element k block by TMA (128-byte swizzle) and
+//               tiled block scales by bulk copies
+//   warp 1      tensor memory, scale copies shared -> tensor memory, MMAs
+//   warps 2-5   what TMA cannot address: row-major block scales (4 bytes a row
+//               and k step into the 128x4 tiles the MMA wants) and, with
+//               kTma = false, the codes themselves (row strides that are not
+//               multiples of 16 bytes; wgrad's per-group strides)
+//   warps 6-13  epilogue: two warps for each 32-lane quarter, alternate
+//               32-column chunks
+// Tensor memory holds two 256-column accumulators at columns 0 and 192 that
+// share 64 columns, and 48 columns of scales behind them: the next tile's
+// MMAs start once the shared columns of this one have been read, which the
+// epilogue does first.
+//
+// Every wait is bounded. After a give-up the roles leave their loops, wait
+// (bounded) for what is in flight, and the status is reported where the call
+// has a status word.
+#pragma once
+
+#include <cuda.h>
+
+#include "group_cast.cuh"
+#include "post_scale.cuh"
+#include "routing.cuh"
+
+namespace nvfp4rs {
+
+enum GemmMode : int { kGemmPlain = 0, kGemmGated = 1, kGemmWgrad = 2, kGemmAdapter = 3 };
+
+constexpr int kGThreads = 448;       // 1 TMA + 1 MMA + 4 loader + 8 epilogue warps
+constexpr int kGLoadWarp = 2;
+constexpr int kGEpiWarp = 6;
+constexpr int kGEpiWarps = 8;
+constexpr int kGI = 128;             // I rows (accumulator lanes) of a tile
+constexpr int kGJ = 256;             // most J rows (accumulator columns) of a tile
+constexpr int kGK = 256;             // contraction elements of a stage: 128 bytes a row
+constexpr int kGStages = 4;
+constexpr int kGBoxJ = 32;           // J rows of one TMA box
+constexpr int kGIBytes = kGI * 128;
+constexpr int kGJBytes = kGJ * 128;
+constexpr int kGScaleTile = 512;     // 128 rows x 4 scales
+constexpr int kGDataBytes = kGIBytes + kGJBytes;      // gated: two I tiles and half the J rows
+constexpr int kGSfBytes = 3 * 4 * kGScaleTile;        // I, and two blocks of 128 J rows, 4 k steps
+constexpr int kGStageBytes = kGDataBytes + kGSfBytes;
+constexpr int kGAcc1 = 192;          // first column of the second accumulator
+constexpr int kGSfCol = 448;         // first scale column
+constexpr int kGLoadLag = 2;         // loader stages in flight before the oldest is published
+
+struct GemmOperand {
+  const uint8_t* data;
+  const uint8_t* scale;
+  const float* s2;
+  int32_t tiled;  // block scales in 128x4 tiles
+};
+
+struct GemmArgs {
+  GemmOperand i, j;
+  int32_t ni;        // output columns: I rows of a group (gated: of each half)
+  int32_t nj;        // wgrad: J rows of a group
+  int32_t K;         // contraction (wgrad: the group's rows instead)
+  int32_t jt;        // J rows of a tile, a multiple of 16
+  int32_t loaders;   // nonzero: warps 2-5 take part
+  int32_t producer;  // nonzero: warp 0 takes part
+  int32_t out_f32;
+  void* out;         // [J rows][ni]
+  uint16_t* pre;     // gated: bf16 [rows][2 ni] or null
+  // adapters
+  const float* u;          // [rows][rank], already scaled
+  const int32_t* ids;      // [rows]
+  const uint16_t* b;       // bf16 [adapters][ni][rank]
+  int32_t rank, adapters;
+};
+
+struct GemmSmem {
+  uint8_t stage[kGStages][kGStageBytes];
+  uint64_t full[kGStages];
+  uint64_t empty[kGStages];
+  uint64_t acc_full;
+  uint64_t acc_free;
+  uint64_t drain;
+  uint32_t tmem;
+  uint32_t gave_up;
+  RoutingSmem routing;
+};
+
+constexpr size_t gemm_smem_bytes(int E) {
+  return ((sizeof(GemmSmem) + 15) & ~size_t{15}) + sizeof(int32_t) * (static_cast<size_t>(E) + 1);
+}
+
+// ------------------------------------------------------------------ tcgen05
+
+// Shared-memory matrix descriptor, K-major, 128-byte swizzle: rows of 128
+// bytes, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t mma_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (uint64_t{1} << 16) | (uint64_t{1024 >> 4} << 32) |
+         (uint64_t{1} << 46) | (uint64_t{2} << 61);
+}
+// Descriptor of a 512-byte scale tile (32 rows of 16 bytes, no swizzle): 8-row
+// groups 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (uint64_t{1} << 16) | (uint64_t{128 >> 4} << 32) |
+         (uint64_t{1} << 46);
+}
+// Instruction descriptor of kind mxf4nvf4: E2M1 x E2M1, UE4M3 scales, M = 128,
+// N = n (a multiple of 16), both operands K-major.
+__device__ __forceinline__ uint32_t mma_idesc(int n) {
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 27);
+}
+
+__device__ __forceinline__ void mma_nvf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                         uint32_t sfb, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 consecutive accumulator columns of the warp's 32 lanes (not yet waited for)
+__device__ __forceinline__ void tmem_load32(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+        "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr));
+}
+// the registers pass through it, so that no use of them is scheduled before it
+__device__ __forceinline__ void tmem_load_wait(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                 "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
+                 "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
+                 "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
+}
+
+// --------------------------------------------------------------- cp.async
+
+// 4, 8 or 16 bytes global -> shared of which the first `valid` are read and
+// the rest zeroed; `src` is a real address even when valid == 0
+template <int kBytes>
+__device__ __forceinline__ void cp_async(uint32_t dst, const uint8_t* src, int valid) {
+  if (!NVFP4_LOAD_OK(src, valid > 0 ? valid : 0)) valid = 0;
+  if (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(valid)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+
+// --------------------------------------------------------------- tile walk
+
+struct GemmTile {
+  int32_t kc;       // contraction length
+  int32_t i0, j0;   // first I and J row inside the group's matrices
+  int32_t iv, jv;   // I and J rows of the tile (iv <= 128, jv <= jt)
+  int64_t irow;     // first I row: in the stacked matrix, or (wgrad) in the s2 vector
+  int64_t jrow;     // first J row, likewise; also the output row
+  int64_t goff;     // wgrad: the group's first routed row
+};
+
+// Forward-only walk: seek(t) for increasing t.
+template <int kMode>
+struct GemmWalk {
+  const RoutingSmem& rs;
+  const GemmArgs& a;
+  int32_t g = 0;
+  int64_t before = 0;  // tiles of the groups before g
+  __device__ __forceinline__ GemmWalk(const RoutingSmem& r, const GemmArgs& x) : rs(r), a(x) {}
+
+  __device__ __forceinline__ bool seek(int64_t t, GemmTile& tile) {
+    const int32_t it = (a.ni + kGI - 1) / kGI;
+    int32_t m = 0;
+    for (; g < rs.E; g++) {
+      m = rs.off[g + 1] - rs.off[g];
+      const int64_t n = static_cast<int64_t>(((kMode == kGemmWgrad ? a.nj : m) + a.jt - 1) / a.jt) * it;
+      if (t < before + n) break;
+      before += n;
+    }
+    if (g >= rs.E) return false;
+    const int32_t local = static_cast<int32_t>(t - before);
+    const int32_t jb = local / it, ib = local - jb * it;
+    const int32_t jn = kMode == kGemmWgrad ? a.nj : m;
+    tile.kc = kMode == kGemmWgrad ? m : a.K;
+    tile.i0 = ib * kGI;
+    tile.j0 = jb * a.jt;
+    tile.iv = min(kGI, a.ni - tile.i0);
+    tile.jv = min(a.jt, jn - tile.j0);
+    tile.goff = rs.off[g];
+    const int64_t in = kMode == kGemmGated ? int64_t{2} * a.ni : a.ni;
+    tile.irow = g * in + tile.i0;
+    tile.jrow = (kMode == kGemmWgrad ? static_cast<int64_t>(g) * a.nj : tile.goff) + tile.j0;
+    return true;
+  }
+};
+
+// ------------------------------------------------------------- loader roles
+
+// Row r of a k block's codes (kcopy: 16 or 8 bytes a copy) and its swizzled place.
+template <int kCopy>
+__device__ __forceinline__ void load_codes(uint32_t dst, const uint8_t* data, int64_t row_bytes, int rows, int valid,
+                                           int32_t kbyte, int tid) {
+  constexpr int kPer = 128 / kCopy;
+  for (int c = tid; c < rows * kPer; c += 128) {
+    const int r = c / kPer, o = (c % kPer) * kCopy;
+    int n = 0;
+    const uint8_t* src = data;
+    if (r < valid) {
+      const int64_t at = static_cast<int64_t>(kbyte) + o;
+      n = static_cast<int>(min(static_cast<int64_t>(kCopy), max(row_bytes - at, int64_t{0})));
+      if (n > 0) src = data + r * row_bytes + at;
+    }
+    cp_async<kCopy>(dst + r * 128 + ((((o >> 4) ^ (r & 7)) << 4) | (o & 15)), src, n);
+  }
+}
+
+// Row-major block scales of `rows` rows and one k block (16 scales a row) into
+// 128x4 tiles: scale (r, 4 k + b) at tile k of the 128-row block, byte
+// (r % 32) * 16 + (r / 32) * 4 + b. Tile k of block q is tile q * 4 + k.
+__device__ __forceinline__ void load_scales(uint8_t* dst, const uint8_t* scale, int32_t cols, int rows, int32_t first,
+                                            int tid) {
+  for (int r = tid; r < rows; r += 128) {
+    uint8_t* d = dst + (r >> 7) * (4 * kGScaleTile) + (r & 31) * 16 + ((r & 127) >> 5) * 4;
+    const uint8_t* s = scale + static_cast<int64_t>(r) * cols + first;
+    if ((cols & 3) == 0) {
+      const uint32_t da = smem_addr(d);
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        const bool in = first + 4 * k < cols;
+        cp_async<4>(da + k * kGScaleTile, in ? s + 4 * k : scale, in ? 4 : 0);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int b = 0; b < 4; b++)
+          if (first + 4 * k + b < cols) w |= static_cast<uint32_t>(gload(s + 4 * k + b)) << (8 * b);
+        *reinterpret_cast<uint32_t*>(d + k * kGScaleTile) = w;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+
+// ------------------------------------------------------------------ kernel
+
+template <class Routing, int kMode, bool kTma>
+__global__ void __launch_bounds__(kGThreads, 1)
+group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant__ CUtensorMap imap,
+                  const __grid_constant__ CUtensorMap jmap, const __grid_constant__ GemmArgs a) {
+  constexpr bool kGated = kMode == kGemmGated;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  GemmSmem& sm = *reinterpret_cast<GemmSmem*>(base);
+  int32_t* off = reinterpret_cast<int32_t*>(base + ((sizeof(GemmSmem) + 15) & ~size_t{15}));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kGStages; s++) {
+      mbar_init(&sm.full[s], (a.producer ? 1 : 0) + (a.loaders ? 4 : 0));
+      mbar_init(&sm.empty[s], 1);
+    }
+    mbar_init(&sm.acc_full, 1);
+    mbar_init(&sm.acc_free, kGEpiWarps);
+    mbar_init(&sm.drain, 1);
+    sm.gave_up = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sm.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  routing.load(sm.routing, off);  // ends with a __syncthreads
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sm.tmem);
+
+  // stage layout: I codes (gated: gate then up), J codes, I scales (likewise), J scales
+  constexpr int kIData = kGated ? 2 * kGIBytes : kGIBytes;
+  constexpr int kISf = (kGated ? 2 : 1) * 4 * kGScaleTile;
+
+  if (sm.routing.ok) {
+    if (warp == 0 && a.producer) {
+      if (lane == 0) {
+        GemmWalk<kMode> walk(sm.routing, a);
+        GemmTile t;
+        uint32_t n = 0;
+        bool ok = true;
+        for (int64_t ti = blockIdx.x; ok && walk.seek(ti, t); ti += gridDim.x) {
+          const int nkb = (t.kc + kGK - 1) / kGK;
+          const int boxes = (t.jv + kGBoxJ - 1) / kGBoxJ;
+          for (int kb = 0; kb < nkb; kb++, n++) {
+            const int s = n % kGStages;
+            if (!mbar_wait(&sm.empty[s], ((n / kGStages) & 1) ^ 1)) {
+              ok = false;
+              break;
+            }
+            uint8_t* st = sm.stage[s];
+            const int ksteps = min(4, (t.kc - kb * kGK + 63) / 64);
+            const int jblocks = (t.jv + 127) / 128;
+            uint32_t bytes = 0;
+            if (kTma) bytes += (kGated ? 2 : 1) * kGIBytes + boxes * kGBoxJ * 128;
+            if (a.i.tiled) bytes += (kGated ? 2 : 1) * ksteps * kGScaleTile;
+            if (a.j.tiled) bytes += jblocks * ksteps * kGScaleTile;
+            mbar_expect_tx(&sm.full[s], bytes);
+            const uint64_t pol = policy_evict_normal();
+            if (kTma) {
+              tma_load_2d(st, &imap, kb * 128, static_cast<int>(t.irow), &sm.full[s], pol);
+              if (kGated) tma_load_2d(st + kGIBytes, &imap, kb * 128, static_cast<int>(t.irow + a.ni), &sm.full[s], pol);
+              for (int b = 0; b < boxes; b++)
+                tma_load_2d(st + kIData + b * kGBoxJ * 128, &jmap, kb * 128, static_cast<int>(t.jrow) + b * kGBoxJ,
+                            &sm.full[s], pol);
+            }
+            // tiled scales: tile (row block, k step) at (block * kc/64 + step) * 512
+            uint8_t* sf = st + kGDataBytes;
+            const int64_t kt = t.kc / 64;
+            if (a.i.tiled) {
+              const uint8_t* src = a.i.scale + (kMode == kGemmWgrad ? t.goff * a.ni / 16 + t.i0 / 128 * kt * kGScaleTile
+                                                                    : t.irow / 128 * kt * kGScaleTile) +
+                                   kb * 4 * kGScaleTile;
+              bulk_load(sf, src, ksteps * kGScaleTile, &sm.full[s]);
+              if (kGated) bulk_load(sf + 4 * kGScaleTile, src + a.ni / 128 * kt * kGScaleTile, ksteps * kGScaleTile, &sm.full[s]);
+            }
+            if (a.j.tiled) {
+              const uint8_t* src = a.j.scale + (kMode == kGemmWgrad ? t.goff * a.nj / 16 + t.j0 / 128 * kt * kGScaleTile
+                                                                    : t.jrow / 128 * kt * kGScaleTile) +
+                                   kb * 4 * kGScaleTile;
+              for (int b = 0; b < jblocks; b++)
+                bulk_load(sf + kISf + b * 4 * kGScaleTile, src + b * kt * kGScaleTile, ksteps * kGScaleTile, &sm.full[s]);
+            }
+          }
+        }
+        if (!ok) {
+          sm.gave_up = 1;
+          for (uint32_t k = n > kGStages ? n - kGStages : 0; k < n; k++)
+            mbar_wait(&sm.full[k % kGStages], (k / kGStages) & 1);
+        }
+      }
+    } else if (warp == 1) {
+      if (lane == 0) {
+        GemmWalk<kMode> walk(sm.routing, a);
+        GemmTile t;
+        uint32_t n = 0, tiles = 0;
+        bool ok = true;
+        for (int64_t ti = blockIdx.x; ok && walk.seek(ti, t); ti += gridDim.x) {
+          const int nkb = (t.kc + kGK - 1) / kGK;
+          if (nkb == 0) continue;
+          if (tiles > 0 && !mbar_wait(&sm.acc_free, (tiles - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t acc = tmem + ((tiles & 1) ? kGAcc1 : 0);
+          const int cols = (t.jv + 15) & ~15;
+          const uint32_t idesc = mma_idesc(cols);
+          const int jblocks = (cols + 127) / 128;
+          const uint32_t sfi = tmem + kGSfCol, sfj = sfi + (kGated ? 32 : 16);
+          for (int kb = 0; kb < nkb; kb++, n++) {
+            const int s = n % kGStages;
+            if (!mbar_wait(&sm.full[s], (n / kGStages) & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const int ksteps = min(4, (t.kc - kb * kGK + 63) / 64);
+            const uint32_t st = smem_addr(sm.stage[s]);
+            const uint32_t sf = st + kGDataBytes;
+            const uint64_t di = mma_desc(st), dj = mma_desc(st + kIData);
+            for (int k = 0; k < ksteps; k++) {
+              tmem_copy_scales(sfi + 4 * k, scale_desc(sf + k * kGScaleTile));
+              if (kGated) tmem_copy_scales(sfi + 16 + 4 * k, scale_desc(sf + (4 + k) * kGScaleTile));
+              tmem_copy_scales(sfj + (kGated ? 4 : 8) * k, scale_desc(sf + kISf + k * kGScaleTile));
+              if (!kGated && jblocks > 1)
+                tmem_copy_scales(sfj + 8 * k + 4, scale_desc(sf + kISf + (4 + k) * kGScaleTile));
+            }
+            for (int k = 0; k < ksteps; k++) {
+              const bool accumulate = kb > 0 || k > 0;
+              mma_nvf4(acc, di + 2 * k, dj + 2 * k, idesc, sfi + 4 * k, sfj + (kGated ? 4 : 8) * k, accumulate);
+              if (kGated)
+                mma_nvf4(acc + 128, di + (kGIBytes >> 4) + 2 * k, dj + 2 * k, idesc, sfi + 16 + 4 * k, sfj + 4 * k,
+                         accumulate);
+            }
+            mma_commit(&sm.empty[s]);
+          }
+          if (ok) mma_commit(&sm.acc_full);
+          tiles++;
+        }
+        if (!ok) {
+          sm.gave_up = 1;
+          mma_commit(&sm.drain);
+          mbar_wait(&sm.drain, 0);
+        }
+      }
+    } else if (warp >= kGLoadWarp && warp < kGEpiWarp && a.loaders) {
+      const int tid = threadIdx.x - kGLoadWarp * 32;
+      GemmWalk<kMode> walk(sm.routing, a);
+      GemmTile t;
+      uint32_t n = 0;
+      bool ok = true;
+      auto publish = [&](uint32_t k) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.full[k % kGStages]);
+      };
+      for (int64_t ti = blockIdx.x; ok && walk.seek(ti, t); ti += gridDim.x) {
+        const int nkb = (t.kc + kGK - 1) / kGK;
+        const int64_t row_bytes = t.kc / 2;
+        const int32_t scols = t.kc / 16;
+        // base addresses of the tile's rows
+        const uint8_t *ic, *jc, *is, *js;
+        if (kMode == kGemmWgrad) {
+          ic = a.i.data + t.goff * a.ni / 2 + t.i0 * row_bytes;
+          jc = a.j.data + t.goff * a.nj / 2 + t.j0 * row_bytes;
+          is = a.i.scale + t.goff * a.ni / 16 + static_cast<int64_t>(t.i0) * scols;
+          js = a.j.scale + t.goff * a.nj / 16 + static_cast<int64_t>(t.j0) * scols;
+        } else {
+          ic = a.i.data + t.irow * row_bytes;
+          jc = a.j.data + t.jrow * row_bytes;
+          is = a.i.scale + t.irow * scols;
+          js = a.j.scale + t.jrow * scols;
+        }
+        for (int kb = 0; kb < nkb; kb++, n++) {
+          const int s = n % kGStages;
+          if (!mbar_wait(&sm.empty[s], ((n / kGStages) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = sm.stage[s];
+          if (!kTma) {
+            const uint32_t d = smem_addr(st);
+            const int cols = (t.jv + 15) & ~15;
+            if (row_bytes % 16 == 0) {
+              load_codes<16>(d, ic, row_bytes, kGI, t.iv, kb * 128, tid);
+              if (kGated) load_codes<16>(d + kGIBytes, ic + a.ni * row_bytes, row_bytes, kGI, t.iv, kb * 128, tid);
+              load_codes<16>(d + kIData, jc, row_bytes, cols, t.jv, kb * 128, tid);
+            } else {
+              load_codes<8>(d, ic, row_bytes, kGI, t.iv, kb * 128, tid);
+              if (kGated) load_codes<8>(d + kGIBytes, ic + a.ni * row_bytes, row_bytes, kGI, t.iv, kb * 128, tid);
+              load_codes<8>(d + kIData, jc, row_bytes, cols, t.jv, kb * 128, tid);
+            }
+          }
+          uint8_t* sf = st + kGDataBytes;
+          if (!a.i.tiled) {
+            load_scales(sf, is, scols, t.iv, kb * 16, tid);
+            if (kGated) load_scales(sf + 4 * kGScaleTile, is + static_cast<int64_t>(a.ni) * scols, scols, t.iv, kb * 16, tid);
+          }
+          if (!a.j.tiled) load_scales(sf + kISf, js, scols, t.jv, kb * 16, tid);
+          cp_async_commit();
+          if (n >= kGLoadLag) {
+            cp_async_wait<kGLoadLag>();
+            publish(n - kGLoadLag);
+          }
+        }
+      }
+      cp_async_wait<0>();
+      if (ok) {
+        for (uint32_t k = n > kGLoadLag ? n - kGLoadLag : 0; k < n; k++) publish(k);
+      } else {
+        sm.gave_up = 1;
+      }
+    } else if (warp >= kGEpiWarp) {
+      const int q = warp & 3;                       // accumulator lanes 32q .. 32q+31
+      const int half = (warp - kGEpiWarp) >> 2;     // chunks of parity `half`
+      GemmWalk<kMode> walk(sm.routing, a);
+      GemmTile t;
+      uint32_t tiles = 0;
+      for (int64_t ti = blockIdx.x; walk.seek(ti, t); ti += gridDim.x) {
+        const bool empty = t.kc == 0;
+        const int il = 32 * q + lane;
+        const bool live = il < t.iv;
+        const int64_t n = t.i0 + il;
+        float si = 0.0f, su = 0.0f;
+        if (live && !empty) {
+          si = gload(&a.i.s2[t.irow + il]);
+          if (kGated) su = gload(&a.i.s2[t.irow + a.ni + il]);
+        }
+        if (!empty) {
+          if (!mbar_wait(&sm.acc_full, tiles & 1)) {
+            if (lane == 0) sm.gave_up = 1;
+            break;
+          }
+          tc_fence_after();
+        }
+        const int set = tiles & 1;
+        const uint32_t acc = tmem + (set ? kGAcc1 : 0) + (static_cast<uint32_t>(32 * q) << 16);
+        // chunks of 32 columns; the first one a warp takes holds its part of
+        // the columns both accumulators share (set 0: the last two, set 1: the
+        // first two; gated: of the up or the gate half)
+        constexpr int kChunks = kGated ? 4 : 8;
+        bool freed = empty;
+        auto release = [&] {
+          if (!freed) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.acc_free);
+            freed = true;
+          }
+        };
+        for (int ci = 0; ci < kChunks / 2; ci++) {
+          const int c = (set == 0 ? (ci == 0 ? kChunks - 2 : 2 * (ci - 1)) : 2 * ci) + half;
+          const int c0 = c * 32;
+          if (c0 >= t.jv) {
+            if (ci == 0) release();
+            continue;
+          }
+          uint32_t v[32], w[32];
+          if (empty) {
+#pragma unroll
+            for (int k = 0; k < 32; k++) v[k] = w[k] = 0;
+          } else {
+            tmem_load32(acc + c0, v);
+            if (kGated) tmem_load32(acc + 128 + c0, w);
+            tmem_load_wait(v);
+            if (kGated) tmem_load_wait(w);
+          }
+          if (ci == 0) release();
+          const int nc = min(32, t.jv - c0);
+          const int64_t row = t.jrow + c0;
+          const float sj = lane < nc && !empty ? gload(&a.j.s2[row + lane]) : 0.0f;
+          if (kGated) {
+            uint16_t* h = static_cast<uint16_t*>(a.out) + row * a.ni + n;
+            uint16_t* p = a.pre + row * (2 * static_cast<int64_t>(a.ni)) + n;
+#pragma unroll
+            for (int k = 0; k < 32; k++) {
+              const float s = __shfl_sync(0xFFFFFFFFu, sj, k);
+              const float gate = __uint_as_float(v[k]) * s * si, up = __uint_as_float(w[k]) * s * su;
+              if (k < nc && live) {
+                gstore(h, static_cast<uint16_t>(bf16x2_rn(silu(gate) * up, 0.0f)));
+                if (a.pre != nullptr) {
+                  const uint32_t b = bf16x2_rn(gate, up);
+                  gstore(p, static_cast<uint16_t>(b));
+                  gstore(p + a.ni, static_cast<uint16_t>(b >> 16));
+                }
+              }
+              h += a.ni;
+              p += 2 * static_cast<int64_t>(a.ni);
+            }
+          } else {
+            float* f = static_cast<float*>(a.out) + row * a.ni + n;
+            uint16_t* h = static_cast<uint16_t*>(a.out) + row * a.ni + n;
+#pragma unroll
+            for (int k = 0; k < 32; k++) {
+              const float y = __uint_as_float(v[k]) * __shfl_sync(0xFFFFFFFFu, sj, k) * si;
+              if (k < nc && live) {
+                if (a.out_f32)
+                  gstore(f, y);
+                else
+                  gstore(h, static_cast<uint16_t>(bf16x2_rn(y, 0.0f)));
+              }
+              f += a.ni;
+              h += a.ni;
+            }
+          }
+        }
+        if (!empty) tiles++;
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+  if (threadIdx.x == 0 && sm.gave_up) routing.report(NVFP4_ERR_TIMEOUT);
+}
+
+}  // namespace nvfp4rs

@@ -106,10 +106,6 @@ __device__ __forceinline__ uint32_t claim(uint32_t* counter) {
   return NVFP4_STORE_OK(counter, 4) ? atomicAdd(counter, 1u) : 0xFFFFFFFFu;
 }
 
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-
 // Non-blocking: has the phase with parity `phase` completed?
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t phase) {
   uint32_t done;

@@ -27,6 +27,7 @@
 #include "dequant.cuh"
 #include "post_scale.cuh"
 #include "mx_cast.cuh"
+#include "group_gemm.cuh"
 
 using namespace nvfp4rs;
 
@@ -577,6 +578,172 @@ nvfp4_status quantize_two_launches(const HostRouting& routing, const void* x, in
   return launch_cast(routing, x, rows, K, E, ra, ca, out, do_col, stream);
 }
 
+// ------------------------------------------------ products (group_gemm.cuh)
+
+// An operand [rows, cols]: every buffer with a nonzero size must be set. With
+// tiled scales its matrices are `unit` rows each (a multiple of 128, checked
+// by the caller where it is a routing) and cols % 128 == 0.
+nvfp4_status check_matrix(const nvfp4_matrix* m, int64_t rows, int64_t cols, int64_t unit) {
+  if (m == nullptr) return NVFP4_ERR_INVALID_ARG;
+  if (m->scale_layout != NVFP4_SCALE_COMPACT && m->scale_layout != NVFP4_SCALE_TILED_128X4)
+    return NVFP4_ERR_INVALID_ARG;
+  if (rows > 0 && cols > 0 && (m->data == nullptr || m->scale == nullptr || m->s2 == nullptr))
+    return NVFP4_ERR_INVALID_ARG;
+  if (m->scale_layout == NVFP4_SCALE_TILED_128X4 && (unit % kRows != 0 || cols % kRows != 0))
+    return NVFP4_ERR_UNSUPPORTED;
+  if (!aligned(m->data, 16) || !aligned(m->scale, 16) || !aligned(m->s2, 4)) return NVFP4_ERR_UNSUPPORTED;
+  return NVFP4_OK;
+}
+
+// Sizes of a product: x [rows, K], E weight matrices [n_rows, K], n_out output columns.
+nvfp4_status check_product(int64_t rows, int64_t K, int32_t E, int64_t n_rows, const void* out) {
+  if (rows < 0 || K < 0 || E < 0 || n_rows < 0) return NVFP4_ERR_INVALID_ARG;
+  if (K % 16 != 0 || n_rows % 16 != 0) return NVFP4_ERR_INVALID_ARG;
+  if (rows > 0 && n_rows > 0 && out == nullptr) return NVFP4_ERR_INVALID_ARG;
+  constexpr int64_t kMaxDim = int64_t{1} << 30;
+  if (E > NVFP4_MAX_GROUPS || rows > kMaxRows || K > kMaxDim || n_rows > kMaxDim) return NVFP4_ERR_UNSUPPORTED;
+  if (n_rows > 0 && E > kMaxRows / n_rows) return NVFP4_ERR_UNSUPPORTED;
+  if (!aligned(out, 16)) return NVFP4_ERR_UNSUPPORTED;
+  return NVFP4_OK;
+}
+
+// TMA descriptor of codes [rows, K/2] bytes: boxes of 128 bytes x box_rows,
+// 128-byte swizzle. K % 32 == 0 (the row stride is a multiple of 16 bytes).
+bool code_tensor_map(CUtensorMap* map, const void* data, int64_t rows, int64_t K, int box_rows) {
+  std::memset(map, 0, sizeof(*map));
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
+  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(data), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tiles of a launch with `jt` J rows a tile: exact for host splits, an upper
+// bound for device routing.
+int64_t product_tiles(const HostRouting& r, int64_t, int64_t nj, int64_t it, int64_t jt, bool wgrad) {
+  int64_t n = 0;
+  for (int32_t g = 0; g < r.E; g++) n += ((wgrad ? nj : r.off[g + 1] - r.off[g]) + jt - 1) / jt * it;
+  return n;
+}
+int64_t product_tiles(const DeviceRouting& r, int64_t rows, int64_t nj, int64_t it, int64_t jt, bool wgrad) {
+  return wgrad ? r.E * ((nj + jt - 1) / jt) * it : (rows / jt + std::min<int64_t>(rows, r.E)) * it;
+}
+
+// `i_rows`, `j_rows`: rows of the two stacked operands (for the tensor maps and
+// the debug build's ranges); a: everything but jt, loaders, producer.
+template <int kMode, class Routing>
+nvfp4_status launch_gemm(const Routing& routing, GemmArgs a, int64_t rows, int64_t i_rows, int64_t j_rows,
+                         cudaStream_t stream) {
+  constexpr bool kWgrad = kMode == kGemmWgrad;
+  const int32_t E = routing.E;
+  const int64_t it = (a.ni + kGI - 1) / kGI;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return NVFP4_ERR_CUDA;
+  // J rows of a tile: the most that fit, halved while there are fewer tiles than SMs
+  const int jt_least = a.j.tiled ? 128 : 32;
+  a.jt = kMode == kGemmGated ? kGJ / 2 : kGJ;
+  int64_t tiles = product_tiles(routing, rows, a.nj, it, a.jt, kWgrad);
+  while (a.jt > jt_least && tiles < sms) {
+    a.jt /= 2;
+    tiles = product_tiles(routing, rows, a.nj, it, a.jt, kWgrad);
+  }
+  if (tiles == 0) return NVFP4_OK;
+  if (tiles > INT32_MAX) return NVFP4_ERR_UNSUPPORTED;
+  const bool tma = !kWgrad && a.K % 32 == 0 && a.K > 0;
+  a.loaders = !tma || !a.i.tiled || !a.j.tiled;
+  a.producer = tma || a.i.tiled || a.j.tiled;
+  CUtensorMap imap, jmap;
+  std::memset(&imap, 0, sizeof(imap));
+  std::memset(&jmap, 0, sizeof(jmap));
+  if (tma && (!code_tensor_map(&imap, a.i.data, i_rows, a.K, kGI) ||
+              !code_tensor_map(&jmap, a.j.data, j_rows, a.K, kGBoxJ)))
+    return NVFP4_ERR_CUDA;
+  auto kernel = group_gemm_kernel<Routing, kMode, !kWgrad>;
+  if (!tma) kernel = group_gemm_kernel<Routing, kMode, false>;
+  const size_t smem = gemm_smem_bytes(E) + 1024;  // + room to align the block to 1024 bytes
+  static_assert(gemm_smem_bytes(NVFP4_MAX_GROUPS) + 1024 <= 227 * 1024, "product kernel shared memory");
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return NVFP4_ERR_CUDA;
+#ifdef NVFP4_CHECK_BOUNDS
+  {
+    const size_t in = static_cast<size_t>(i_rows) * (kWgrad ? 0 : a.K), jn = static_cast<size_t>(j_rows) * (kWgrad ? 0 : a.K);
+    const size_t ib = kWgrad ? static_cast<size_t>(rows) * a.ni : in, jb = kWgrad ? static_cast<size_t>(rows) * a.nj : jn;
+    const size_t out = static_cast<size_t>(kWgrad ? j_rows : rows) * a.ni;
+    NVFP4_SPANS(SpanList{}
+                    .add(a.j.data, jb / 2, false)
+                    .add(a.i.data, ib / 2, false)
+                    .add(a.i.scale, ib / 16, false)
+                    .add(a.j.scale, jb / 16, false)
+                    .add(a.i.s2, 4 * static_cast<size_t>(i_rows), false)
+                    .add(a.j.s2, 4 * static_cast<size_t>(j_rows), false)
+                    .routing(routing)
+                    .add(a.out, out * (a.out_f32 ? 4 : 2), true)
+                    .add(a.pre, out * 4, true)
+                    .set(stream));
+  }
+#endif
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, sms)));
+  cfg.blockDim = dim3(kGThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, routing, imap, jmap, a));
+}
+
+GemmOperand operand(const nvfp4_matrix* m) {
+  return GemmOperand{m->data, m->scale, m->s2, m->scale_layout == NVFP4_SCALE_TILED_128X4};
+}
+
+nvfp4_status check_gemm(const nvfp4_matrix* x, int64_t rows, int64_t K, int32_t E, const nvfp4_matrix* w, int64_t n_rows,
+                        int64_t unit, const void* out) {
+  nvfp4_status s = check_product(rows, K, E, n_rows, out);
+  if (s == NVFP4_OK) s = check_matrix(x, rows, K, kRows);
+  if (s == NVFP4_OK) s = check_matrix(w, E * n_rows, K, unit);
+  return s;
+}
+
+GemmArgs gemm_args(const nvfp4_matrix* x, int64_t K, const nvfp4_matrix* w, int64_t N, void* out, bool f32) {
+  GemmArgs a{};
+  a.i = operand(w);
+  a.j = operand(x);
+  a.ni = static_cast<int32_t>(N);
+  a.K = static_cast<int32_t>(K);
+  a.out = out;
+  a.out_f32 = f32;
+  return a;
+}
+
+
+bool out_dtype_ok(int32_t t) { return t == NVFP4_OUT_F32 || t == NVFP4_OUT_BF16; }
+
+// wgrad: J = dy's columns, I = x's columns, the contraction over a group's rows.
+nvfp4_status check_wgrad(const nvfp4_matrix* dy, const nvfp4_matrix* x, int64_t rows, int32_t E, int64_t N, int64_t K,
+                         void* dw, int32_t dw_dtype, GemmArgs& a) {
+  if (!out_dtype_ok(dw_dtype)) return NVFP4_ERR_INVALID_ARG;
+  nvfp4_status s = check_product(E > 0 ? N : 0, N, E, K, dw);  // both widths multiples of 16, E*K rows of I
+  if (s == NVFP4_OK) s = check_product(rows, K, E, N, dw);
+  if (s == NVFP4_OK) s = check_matrix(dy, N, rows, N);
+  if (s == NVFP4_OK) s = check_matrix(x, K, rows, K);
+  if (s != NVFP4_OK) return s;
+  a.i = operand(x);
+  a.j = operand(dy);
+  a.ni = static_cast<int32_t>(K);
+  a.nj = static_cast<int32_t>(N);
+  a.out = dw;
+  a.out_f32 = dw_dtype == NVFP4_OUT_F32;
+  return NVFP4_OK;
+}
+
+int32_t row_unit(const nvfp4_matrix* x, int32_t compact) {
+  return x->scale_layout == NVFP4_SCALE_TILED_128X4 ? kRows : compact;
+}
+
 }  // namespace
 
 extern "C" {
@@ -804,6 +971,99 @@ nvfp4_status nvfp4_row_post_scale(const float* gemm_out, int64_t rows, int64_t c
   cfg.stream = stream;
   return cuda_status(cudaLaunchKernelEx(&cfg, kernel, reinterpret_cast<const float4*>(gemm_out), rows, cols / 4,
                                         row_amax, reinterpret_cast<const float4*>(bias), out));
+}
+
+nvfp4_status nvfp4_group_gemm(const nvfp4_matrix* x, int64_t sum_M, int64_t K, const int64_t* m_splits_host,
+                              int32_t num_groups, const nvfp4_matrix* w, int64_t N, void* y, int32_t y_dtype,
+                              cudaStream_t stream) {
+  if (!out_dtype_ok(y_dtype)) return NVFP4_ERR_INVALID_ARG;
+  nvfp4_status s = check_gemm(x, sum_M, K, num_groups, w, N, N, y);
+  if (s != NVFP4_OK) return s;
+  static thread_local HostRouting routing;
+  s = host_routing(m_splits_host, num_groups, sum_M, routing, row_unit(x, 1));
+  if (s != NVFP4_OK || sum_M == 0 || N == 0) return s;
+  return launch_gemm<kGemmPlain>(routing, gemm_args(x, K, w, N, y, y_dtype == NVFP4_OUT_F32), sum_M, num_groups * N,
+                                 sum_M, stream);
+}
+
+nvfp4_status nvfp4_group_gemm_graphsafe(const nvfp4_matrix* x, int64_t capacity_rows, int64_t K,
+                                        const int64_t* first_dims_dev, const int64_t* tensor_offsets_dev,
+                                        int32_t num_groups, const nvfp4_matrix* w, int64_t N, void* y,
+                                        int32_t y_dtype, int32_t* status_dev, cudaStream_t stream) {
+  if (!out_dtype_ok(y_dtype) || K == 0) return NVFP4_ERR_INVALID_ARG;
+  nvfp4_status s = check_gemm(x, capacity_rows, K, num_groups, w, N, N, y);
+  if (s != NVFP4_OK) return s;
+  DeviceRouting routing;
+  s = device_routing(first_dims_dev, tensor_offsets_dev, status_dev, K, capacity_rows, num_groups, row_unit(x, 1),
+                     routing);
+  if (s != NVFP4_OK) return s;
+  s = cuda_status(cudaMemsetAsync(status_dev, 0, sizeof(int32_t), stream));
+  if (s != NVFP4_OK || capacity_rows == 0 || N == 0) return s;
+  return launch_gemm<kGemmPlain>(routing, gemm_args(x, K, w, N, y, y_dtype == NVFP4_OUT_F32), capacity_rows,
+                                 num_groups * N, capacity_rows, stream);
+}
+
+nvfp4_status nvfp4_group_gated_gemm(const nvfp4_matrix* x, int64_t sum_M, int64_t K, const int64_t* m_splits_host,
+                                    int32_t num_groups, const nvfp4_matrix* w, int64_t F, void* h_bf16,
+                                    void* gate_up_bf16, cudaStream_t stream) {
+  if (F < 0 || F % 16 != 0) return NVFP4_ERR_INVALID_ARG;
+  nvfp4_status s = check_gemm(x, sum_M, K, num_groups, w, 2 * F, F, h_bf16);
+  if (s != NVFP4_OK) return s;
+  if (!aligned(gate_up_bf16, 16)) return NVFP4_ERR_UNSUPPORTED;
+  static thread_local HostRouting routing;
+  s = host_routing(m_splits_host, num_groups, sum_M, routing, row_unit(x, 1));
+  if (s != NVFP4_OK || sum_M == 0 || F == 0) return s;
+  GemmArgs a = gemm_args(x, K, w, F, h_bf16, false);
+  a.pre = static_cast<uint16_t*>(gate_up_bf16);
+  return launch_gemm<kGemmGated>(routing, a, sum_M, num_groups * 2 * F, sum_M, stream);
+}
+
+nvfp4_status nvfp4_group_gated_gemm_graphsafe(const nvfp4_matrix* x, int64_t capacity_rows, int64_t K,
+                                              const int64_t* first_dims_dev, const int64_t* tensor_offsets_dev,
+                                              int32_t num_groups, const nvfp4_matrix* w, int64_t F, void* h_bf16,
+                                              void* gate_up_bf16, int32_t* status_dev, cudaStream_t stream) {
+  if (F < 0 || F % 16 != 0 || K == 0) return NVFP4_ERR_INVALID_ARG;
+  nvfp4_status s = check_gemm(x, capacity_rows, K, num_groups, w, 2 * F, F, h_bf16);
+  if (s != NVFP4_OK) return s;
+  if (!aligned(gate_up_bf16, 16)) return NVFP4_ERR_UNSUPPORTED;
+  DeviceRouting routing;
+  s = device_routing(first_dims_dev, tensor_offsets_dev, status_dev, K, capacity_rows, num_groups, row_unit(x, 1),
+                     routing);
+  if (s != NVFP4_OK) return s;
+  s = cuda_status(cudaMemsetAsync(status_dev, 0, sizeof(int32_t), stream));
+  if (s != NVFP4_OK || capacity_rows == 0 || F == 0) return s;
+  GemmArgs a = gemm_args(x, K, w, F, h_bf16, false);
+  a.pre = static_cast<uint16_t*>(gate_up_bf16);
+  return launch_gemm<kGemmGated>(routing, a, capacity_rows, num_groups * 2 * F, capacity_rows, stream);
+}
+
+nvfp4_status nvfp4_group_wgrad(const nvfp4_matrix* dy, const nvfp4_matrix* x, int64_t sum_M,
+                               const int64_t* m_splits_host, int32_t num_groups, int64_t N, int64_t K, void* dw,
+                               int32_t dw_dtype, cudaStream_t stream) {
+  GemmArgs a{};
+  nvfp4_status s = check_wgrad(dy, x, sum_M, num_groups, N, K, dw, dw_dtype, a);
+  if (s != NVFP4_OK) return s;
+  static thread_local HostRouting routing;
+  s = host_routing(m_splits_host, num_groups, sum_M, routing, std::max(row_unit(x, kBlockRows), row_unit(dy, kBlockRows)));
+  if (s != NVFP4_OK || N == 0 || K == 0 || num_groups == 0) return s;
+  return launch_gemm<kGemmWgrad>(routing, a, sum_M, num_groups * K, num_groups * N, stream);
+}
+
+nvfp4_status nvfp4_group_wgrad_graphsafe(const nvfp4_matrix* dy, const nvfp4_matrix* x, int64_t capacity_rows,
+                                         const int64_t* first_dims_dev, const int64_t* tensor_offsets_dev,
+                                         int32_t num_groups, int64_t N, int64_t K, void* dw, int32_t dw_dtype,
+                                         int32_t* status_dev, cudaStream_t stream) {
+  GemmArgs a{};
+  nvfp4_status s = check_wgrad(dy, x, capacity_rows, num_groups, N, K, dw, dw_dtype, a);
+  if (s != NVFP4_OK) return s;
+  if (K == 0) return NVFP4_ERR_INVALID_ARG;
+  DeviceRouting routing;
+  s = device_routing(first_dims_dev, tensor_offsets_dev, status_dev, K, capacity_rows, num_groups,
+                     std::max(row_unit(x, kBlockRows), row_unit(dy, kBlockRows)), routing);
+  if (s != NVFP4_OK) return s;
+  s = cuda_status(cudaMemsetAsync(status_dev, 0, sizeof(int32_t), stream));
+  if (s != NVFP4_OK || N == 0 || num_groups == 0) return s;
+  return launch_gemm<kGemmWgrad>(routing, a, capacity_rows, num_groups * K, num_groups * N, stream);
 }
 
 nvfp4_status nvfp4_mx_group_cast(const void* x_bf16, int64_t sum_M, int64_t K, const int64_t* m_splits_host,
