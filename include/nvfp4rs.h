@@ -470,6 +470,67 @@ NVFP4RS_API nvfp4_status nvfp4_group_gated_gemm_graphsafe(const nvfp4_matrix* x,
 
 
 /*
+ * Gated feed-forward block, backward of the activation and the product. With
+ * g = gate_up[t][f], u = gate_up[t][F + f] (bf16, as nvfp4_group_gated_gemm
+ * saves them) and s = 1 / (1 + e^-g):
+ *   d_gate_up[t][f]     = dh u s (1 + g (1 - s))
+ *   d_gate_up[t][F + f] = dh g s
+ * in fp32, rounded once to bf16. In the same pass the row amax and the
+ * per-group column amax of d_gate_up, bit-identical to nvfp4_group_amax of it:
+ * the scale sources of its nvfp4_group_cast, after which nvfp4_group_gemm (on
+ * the weights' colwise cast) and nvfp4_group_wgrad finish the backward pass.
+ *   dh         device bf16 [sum_M, F]     gate_up  device bf16 [sum_M, 2F]
+ *   d_gate_up  device bf16 [sum_M, 2F]; may be gate_up itself (in place)
+ *   row_amax   device fp32 [sum_M] or NULL
+ *   col_amax   device fp32 [num_groups*2F] or NULL; zeroed by this call
+ * F % 16 == 0 (else NVFP4_ERR_INVALID_ARG), F <= 65536 and m_g % 16 == 0 (else
+ * NVFP4_ERR_UNSUPPORTED); finite inputs. One launch, or two with col_amax.
+ */
+NVFP4RS_API nvfp4_status nvfp4_group_gated_backward(const void* dh_bf16, const void* gate_up_bf16, int64_t sum_M,
+                                        int64_t F, const int64_t* m_splits_host, int32_t num_groups,
+                                        void* d_gate_up_bf16, float* row_amax, float* col_amax,
+                                        cudaStream_t stream);
+
+/* nvfp4_group_gated_backward with graph-safe routing; tensor_offsets in
+ * elements of gate_up (row offset * 2F). */
+NVFP4RS_API nvfp4_status nvfp4_group_gated_backward_graphsafe(const void* dh_bf16, const void* gate_up_bf16,
+                                                  int64_t capacity_rows, int64_t F, const int64_t* first_dims_dev,
+                                                  const int64_t* tensor_offsets_dev, int32_t num_groups,
+                                                  void* d_gate_up_bf16, float* row_amax, float* col_amax,
+                                                  int32_t* status_dev, cudaStream_t stream);
+
+/* Bytes of workspace of nvfp4_adapter_gemm (0 for arguments it refuses). */
+NVFP4RS_API size_t nvfp4_adapter_workspace_bytes(int64_t rows, int32_t rank);
+
+/*
+ * Low-rank adapters of many requests beside one shared projection:
+ *   y[t] = X[t] W^T + factor[a] (x[t] A_a^T) B_a^T,   a = ids[t]; no second
+ *   term where ids[t] == -1
+ * X, W the NVFP4 operands [rows, K] and [N, K] (x_bf16's rowwise cast and the
+ * shared weights), x, A, B bf16. u = factor (x A^T) is kept in fp32, its second
+ * product added in fp32 to the projection before the one rounding of y.
+ *   x_bf16   device bf16 [rows, K]
+ *   a_bf16   device bf16 [num_adapters, rank, K]
+ *   b_bf16   device bf16 [num_adapters, N, rank]
+ *   factor   device fp32 [num_adapters]
+ *   ids_dev  device int32 [rows], any order; tokens of one request next to each
+ *            other are faster. Read on the device only, so the call can be
+ *            captured and replayed with other ids.
+ *   workspace   device, nvfp4_adapter_workspace_bytes(rows, rank) bytes, owned by
+ *            the caller; calls that share one must be ordered on one stream
+ *   status_dev  device int32 [1]: 0, or NVFP4_ERR_ROUTING when an id is outside
+ *            [-1, num_adapters) (that token gets no adapter)
+ * rank a multiple of 8 (else NVFP4_ERR_INVALID_ARG) up to 64 (else
+ * NVFP4_ERR_UNSUPPORTED). A token's result does not depend on the adapters of
+ * the other tokens. A memset of status and two launches.
+ */
+NVFP4RS_API nvfp4_status nvfp4_adapter_gemm(const void* x_bf16, const nvfp4_matrix* x, int64_t rows, int64_t K,
+                                const nvfp4_matrix* w, int64_t N, const void* a_bf16, const void* b_bf16,
+                                const float* factor, int32_t num_adapters, int32_t rank, const int32_t* ids_dev,
+                                void* y, int32_t y_dtype, void* workspace, size_t workspace_bytes,
+                                int32_t* status_dev, cudaStream_t stream);
+
+/*
  * Per-row FP32 scaling of a GEMM output (TransformerEngine #2931, sequence
  * diagram: the GEMM runs with the row-scaled operand's amax replaced by
  * ones, then its output rows are multiplied by the row-wise amax and

@@ -107,8 +107,14 @@ def lib():
         L.nvfp4_group_gated_gemm_graphsafe.argtypes = [mp, i64, i64, vp, vp, i32, mp, i64, vp, vp, vp, vp]
         L.nvfp4_group_wgrad.argtypes = [mp, mp, i64, vp, i32, i64, i64, vp, i32, vp]
         L.nvfp4_group_wgrad_graphsafe.argtypes = [mp, mp, i64, vp, vp, i32, i64, i64, vp, i32, vp, vp]
+        L.nvfp4_group_gated_backward.argtypes = [vp, vp, i64, i64, vp, i32, vp, vp, vp, vp]
+        L.nvfp4_group_gated_backward_graphsafe.argtypes = [vp, vp, i64, i64, vp, vp, i32, vp, vp, vp, vp, vp]
+        L.nvfp4_adapter_workspace_bytes.argtypes = [i64, i32]
+        L.nvfp4_adapter_workspace_bytes.restype = sz
+        L.nvfp4_adapter_gemm.argtypes = [vp, mp, i64, i64, mp, i64, vp, vp, vp, i32, i32, vp, vp, i32, vp, sz, vp, vp]
         for f in ("nvfp4_group_gemm", "nvfp4_group_gemm_graphsafe", "nvfp4_group_gated_gemm",
-                  "nvfp4_group_gated_gemm_graphsafe", "nvfp4_group_wgrad", "nvfp4_group_wgrad_graphsafe"):
+                  "nvfp4_group_gated_gemm_graphsafe", "nvfp4_group_wgrad", "nvfp4_group_wgrad_graphsafe",
+                  "nvfp4_group_gated_backward", "nvfp4_group_gated_backward_graphsafe", "nvfp4_adapter_gemm"):
             getattr(L, f).restype = ctypes.c_int
         for f in ("nvfp4_group_amax", "nvfp4_group_cast", "nvfp4_group_amax_graphsafe",
                   "nvfp4_group_cast_graphsafe", "nvfp4_dequantize", "nvfp4_group_quantize",
@@ -530,6 +536,79 @@ def nvfp4_group_wgrad_graphsafe(dy: Dict[str, object], x: Dict[str, object], cap
     fd, to, st = _routing(first_dims, tensor_offsets, status, E)
     _on(dev, stream, "nvfp4_group_wgrad_graphsafe", lambda s: lib().nvfp4_group_wgrad_graphsafe(
         ctypes.byref(dm), ctypes.byref(xm), rows, fd, to, E, N, K, wp, dt, st, s))
+
+
+def _gated_backward(dh, gate_up, d_gate_up, row_amax, col_amax, E):
+    rows, F = dh.shape
+    for t, name in ((gate_up, "gate_up"), (d_gate_up, "d_gate_up")):
+        if tuple(t.shape) != (rows, 2 * F):
+            raise ValueError(f"{name} must be [rows, 2F]")
+    for t, n, name in ((row_amax, rows, "row_amax"), (col_amax, E * 2 * F, "col_amax")):
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{name} must have {n} entries")
+    return (rows, F, _dev(dh, torch.bfloat16, "dh"), _dev(gate_up, torch.bfloat16, "gate_up"),
+            _dev(d_gate_up, torch.bfloat16, "d_gate_up"), _dev(row_amax, torch.float32, "row_amax"),
+            _dev(col_amax, torch.float32, "col_amax"))
+
+
+def nvfp4_group_gated_backward(dh: torch.Tensor, gate_up: torch.Tensor, m_splits: Sequence[int],
+                               d_gate_up: torch.Tensor, row_amax: Optional[torch.Tensor] = None,
+                               col_amax: Optional[torch.Tensor] = None, stream=None) -> None:
+    """d_gate_up [rows, 2F] from dh [rows, F] and the saved gate_up [rows, 2F]
+    of nvfp4_group_gated_gemm, with the row amax [rows] and per-group column
+    amax [E*2F] its cast takes. d_gate_up may be gate_up."""
+    arr, E = _splits(m_splits)
+    dev = _same_device(dh, gate_up, d_gate_up, row_amax, col_amax)
+    rows, F, dp, gp, op, rp, cp = _gated_backward(dh, gate_up, d_gate_up, row_amax, col_amax, E)
+    _on(dev, stream, "nvfp4_group_gated_backward", lambda s: lib().nvfp4_group_gated_backward(
+        dp, gp, rows, F, arr, E, op, rp, cp, s))
+
+
+def nvfp4_group_gated_backward_graphsafe(dh: torch.Tensor, gate_up: torch.Tensor, first_dims: Optional[torch.Tensor],
+                                         tensor_offsets: Optional[torch.Tensor], d_gate_up: torch.Tensor,
+                                         status: torch.Tensor, row_amax: Optional[torch.Tensor] = None,
+                                         col_amax: Optional[torch.Tensor] = None, stream=None,
+                                         num_groups: Optional[int] = None) -> None:
+    E = _groups(first_dims, num_groups)
+    dev = _same_device(dh, gate_up, d_gate_up, row_amax, col_amax, first_dims, tensor_offsets, status)
+    rows, F, dp, gp, op, rp, cp = _gated_backward(dh, gate_up, d_gate_up, row_amax, col_amax, E)
+    fd, to, st = _routing(first_dims, tensor_offsets, status, E)
+    _on(dev, stream, "nvfp4_group_gated_backward_graphsafe", lambda s: lib().nvfp4_group_gated_backward_graphsafe(
+        dp, gp, rows, F, fd, to, E, op, rp, cp, st, s))
+
+
+def nvfp4_adapter_workspace_bytes(rows: int, rank: int) -> int:
+    return int(lib().nvfp4_adapter_workspace_bytes(int(rows), int(rank)))
+
+
+def nvfp4_adapter_gemm(x_bf16: torch.Tensor, x: Dict[str, object], w: Dict[str, object], a: torch.Tensor,
+                       b: torch.Tensor, factor: torch.Tensor, ids: torch.Tensor, y: torch.Tensor,
+                       workspace: torch.Tensor, status: torch.Tensor, stream=None) -> None:
+    """y [rows, N] = X W^T + factor[i] (x A_i^T) B_i^T with i = ids[t] (-1: none).
+    x_bf16 [rows, K] and its rowwise cast x, w [N, K], a [L, R, K], b [L, N, R],
+    factor [L], ids int32 [rows]; workspace from alloc_adapter_workspace."""
+    rows, K = x_bf16.shape
+    L, R = a.shape[0], a.shape[1]
+    N = y.shape[1]
+    if y.shape[0] != rows or ids.numel() != rows or factor.numel() != L:
+        raise ValueError("y and ids must have a row for each of x_bf16's, factor an entry for each adapter")
+    if tuple(a.shape) != (L, R, K) or tuple(b.shape) != (L, N, R):
+        raise ValueError("a must be [L, R, K] and b [L, N, R]")
+    dt = _out_dtype(y, "y")
+    dev = _same_device(y, x_bf16, a, b, factor, ids, workspace, status, *_parts(x, w))
+    xm, wm = _matrix(x, rows, rows * K, "x"), _matrix(w, N, N * K, "w")
+    wp, wb = _workspace(workspace)
+    ptrs = (_dev(x_bf16, torch.bfloat16, "x_bf16"), _dev(a, torch.bfloat16, "a"), _dev(b, torch.bfloat16, "b"),
+            _dev(factor, torch.float32, "factor"), _dev(ids, torch.int32, "ids"), _dev(y, y.dtype, "y"),
+            _dev(status, torch.int32, "status"))
+    xp, ap, bp, fp, ip, yp, st = ptrs
+    _on(dev, stream, "nvfp4_adapter_gemm", lambda s: lib().nvfp4_adapter_gemm(
+        xp, ctypes.byref(xm), rows, K, ctypes.byref(wm), N, ap, bp, fp, L, R, ip, yp, dt, wp, wb, st, s))
+
+
+def alloc_adapter_workspace(rows: int, rank: int, device="cuda") -> torch.Tensor:
+    """Workspace of nvfp4_adapter_gemm (uint8, uninitialised)."""
+    return torch.empty(nvfp4_adapter_workspace_bytes(rows, rank), dtype=torch.uint8, device=device)
 
 
 # -------------------------------------------------------- buffer helpers

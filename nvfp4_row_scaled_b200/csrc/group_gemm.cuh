@@ -103,6 +103,7 @@ struct GemmArgs {
   const int32_t* ids;      // [rows]
   const uint16_t* b;       // bf16 [adapters][ni][rank]
   int32_t rank, adapters;
+  int32_t* status;         // or null
 };
 
 struct GemmSmem {
@@ -295,6 +296,59 @@ __device__ __forceinline__ void load_scales(uint8_t* dst, const uint8_t* scale, 
 }
 
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+
+// The adapters' share of a lane's 32 outputs (feature n of rows row .. row + nc - 1):
+// y[k] += sum_r u[row + k][r] b[id][n][r], in fp32, ranks in order in two
+// interleaved sums (even and odd). Rows of one adapter, the rule in a prompt,
+// read the lane's row of B once; other rows read theirs eight ranks at a time,
+// several rows in flight.
+__device__ __forceinline__ void add_adapters(float (&y)[32], const GemmArgs& a, int64_t row, int64_t n, int nc, int lane,
+                                             bool live) {
+  int32_t id = lane < nc ? gload(&a.ids[row + lane]) : -1;
+  if (id < 0 || id >= a.adapters) id = -1;
+  if (!__any_sync(0xFFFFFFFFu, id >= 0)) return;
+  const int32_t id0 = __shfl_sync(0xFFFFFFFFu, id, 0);
+  const bool same = __all_sync(0xFFFFFFFFu, lane >= nc || id == id0);
+  const int64_t nn = live ? n : 0;  // a lane past the features computes on feature 0 and stores nothing
+  const float* u = a.u + row * a.rank;
+  const uint16_t* b = a.b + nn * a.rank;
+  const int64_t pitch = static_cast<int64_t>(a.ni) * a.rank;
+  uint64_t acc[32];
+#pragma unroll
+  for (int k = 0; k < 32; k++) acc[k] = pack2(y[k], 0.0f);
+  auto dot8 = [&](uint64_t& c, const uint4& w, const float* up) {
+    const float4 u0 = gload(reinterpret_cast<const float4*>(up)), u1 = gload(reinterpret_cast<const float4*>(up) + 1);
+    c = fma2x(pack2(u0.x, u0.y), unpack2(w.x), c);
+    c = fma2x(pack2(u0.z, u0.w), unpack2(w.y), c);
+    c = fma2x(pack2(u1.x, u1.y), unpack2(w.z), c);
+    c = fma2x(pack2(u1.z, u1.w), unpack2(w.w), c);
+  };
+  for (int r = 0; r < a.rank; r += 8) {
+    if (same) {
+      const uint4 w = gload(reinterpret_cast<const uint4*>(b + id0 * pitch + r));
+#pragma unroll
+      for (int k = 0; k < 32; k++)
+        if (k < nc) dot8(acc[k], w, u + k * a.rank + r);
+    } else {
+#pragma unroll
+      for (int k0 = 0; k0 < 32; k0 += 4) {
+        uint4 w[4];
+        int32_t ik[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          ik[k] = __shfl_sync(0xFFFFFFFFu, id, k0 + k);
+          if (ik[k] >= 0) w[k] = gload(reinterpret_cast<const uint4*>(b + ik[k] * pitch + r));
+        }
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+          if (ik[k] >= 0) dot8(acc[k0 + k], w[k], u + (k0 + k) * a.rank + r);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 32; k++)
+    y[k] = __uint_as_float(static_cast<uint32_t>(acc[k])) + __uint_as_float(static_cast<uint32_t>(acc[k] >> 32));
+}
 
 // ------------------------------------------------------------------ kernel
 
@@ -536,6 +590,7 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
           }
           tc_fence_after();
         }
+        if (kMode == kGemmAdapter) grid_dependency_wait();  // u comes from the kernel before this one
         const int set = tiles & 1;
         const uint32_t acc = tmem + (set ? kGAcc1 : 0) + (static_cast<uint32_t>(32 * q) << 16);
         // chunks of 32 columns; the first one a warp takes holds its part of
@@ -591,16 +646,19 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
               p += 2 * static_cast<int64_t>(a.ni);
             }
           } else {
+            float y[32];
+#pragma unroll
+            for (int k = 0; k < 32; k++) y[k] = __uint_as_float(v[k]) * __shfl_sync(0xFFFFFFFFu, sj, k) * si;
+            if (kMode == kGemmAdapter) add_adapters(y, a, row, n, nc, lane, live);
             float* f = static_cast<float*>(a.out) + row * a.ni + n;
             uint16_t* h = static_cast<uint16_t*>(a.out) + row * a.ni + n;
 #pragma unroll
             for (int k = 0; k < 32; k++) {
-              const float y = __uint_as_float(v[k]) * __shfl_sync(0xFFFFFFFFu, sj, k) * si;
               if (k < nc && live) {
                 if (a.out_f32)
-                  gstore(f, y);
+                  gstore(f, y[k]);
                 else
-                  gstore(h, static_cast<uint16_t>(bf16x2_rn(y, 0.0f)));
+                  gstore(h, static_cast<uint16_t>(bf16x2_rn(y[k], 0.0f)));
               }
               f += a.ni;
               h += a.ni;
@@ -618,7 +676,10 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
-  if (threadIdx.x == 0 && sm.gave_up) routing.report(NVFP4_ERR_TIMEOUT);
+  if (threadIdx.x == 0 && sm.gave_up) {
+    routing.report(NVFP4_ERR_TIMEOUT);
+    if (kMode == kGemmAdapter && a.status != nullptr) gstore(a.status, static_cast<int32_t>(NVFP4_ERR_TIMEOUT));
+  }
 }
 
 }  // namespace nvfp4rs

@@ -28,6 +28,8 @@
 #include "post_scale.cuh"
 #include "mx_cast.cuh"
 #include "group_gemm.cuh"
+#include "gated_backward.cuh"
+#include "adapter.cuh"
 
 using namespace nvfp4rs;
 
@@ -685,6 +687,10 @@ nvfp4_status launch_gemm(const Routing& routing, GemmArgs a, int64_t rows, int64
                     .routing(routing)
                     .add(a.out, out * (a.out_f32 ? 4 : 2), true)
                     .add(a.pre, out * 4, true)
+                    .add(a.u, 4 * static_cast<size_t>(rows) * a.rank, false)
+                    .add(a.ids, 4 * static_cast<size_t>(rows), false)
+                    .add(a.status, 4, true)
+                    .add(a.b, 2 * static_cast<size_t>(a.adapters) * a.ni * a.rank, false)
                     .set(stream));
   }
 #endif
@@ -693,6 +699,13 @@ nvfp4_status launch_gemm(const Routing& routing, GemmArgs a, int64_t rows, int64
   cfg.blockDim = dim3(kGThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
+  // the adapters' first half is the kernel before this one: its result is
+  // waited for in the epilogue only
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kMode == kGemmAdapter ? 1 : 0;
   return cuda_status(cudaLaunchKernelEx(&cfg, kernel, routing, imap, jmap, a));
 }
 
@@ -742,6 +755,127 @@ nvfp4_status check_wgrad(const nvfp4_matrix* dy, const nvfp4_matrix* x, int64_t 
 
 int32_t row_unit(const nvfp4_matrix* x, int32_t compact) {
   return x->scale_layout == NVFP4_SCALE_TILED_128X4 ? kRows : compact;
+}
+
+// Zeroing (when col_amax is given) and the gradient kernel, launched
+// programmatically after it: its reads overlap the zeroing, its atomics wait.
+template <class Routing>
+nvfp4_status launch_gated_backward(const Routing& routing, const void* dh, const void* gate_up, int64_t rows, int64_t F,
+                                   void* out, float* row_amax, float* col_amax, cudaStream_t stream) {
+  const int64_t n_col = col_amax != nullptr ? 2 * F * routing.E : 0;
+  const int64_t tiles = (rows + kBwRows - 1) / kBwRows;
+  if (n_col == 0 && tiles == 0) return NVFP4_OK;
+  const size_t n = static_cast<size_t>(rows) * static_cast<size_t>(F);
+  NVFP4_SPANS(SpanList{}
+                  .add(dh, 2 * n, false)
+                  .add(gate_up, 4 * n, false)
+                  .routing(routing)
+                  .add(out, 4 * n, true)
+                  .add(row_amax, 4 * static_cast<size_t>(rows), true)
+                  .add(col_amax, 4 * static_cast<size_t>(n_col), true)
+                  .set(stream));
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return NVFP4_ERR_CUDA;
+  if (n_col > 0) {
+    const int64_t blocks = std::min<int64_t>((n_col + 255) / 256, 2 * static_cast<int64_t>(sms));
+    zero_f32_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(col_amax, n_col);
+    const nvfp4_status z = cuda_status(cudaGetLastError());
+    if (z != NVFP4_OK || tiles == 0) return z;
+  }
+  // CTAs a tile: doubled while there are fewer CTAs than two a SM, or while the
+  // column maxima of one CTA pass 64 KB
+  const int64_t chunks = (F + kBwChunk - 1) / kBwChunk;
+  int cn = 1;
+  while (cn < 8 && cn < chunks && (tiles * cn < 2 * sms || (chunks + cn - 1) / cn > 32)) cn *= 2;
+  const int64_t per = (chunks + cn - 1) / cn;
+  if (per > 32) return NVFP4_ERR_UNSUPPORTED;
+  const size_t smem = static_cast<size_t>(per) * 2 * kBwChunk * 4 + sizeof(int32_t) * (routing.E + 1);
+  auto kernel = gated_backward_kernel<Routing>;
+  if (smem > 46 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return NVFP4_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * cn));
+  cfg.blockDim = dim3(kBwThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cn);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = n_col > 0 ? 2 : 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, routing, static_cast<const uint4*>(dh),
+                                        static_cast<const uint4*>(gate_up), static_cast<uint4*>(out),
+                                        static_cast<int32_t>(F), static_cast<int32_t>(cn), row_amax, col_amax));
+}
+
+nvfp4_status check_gated_backward(const void* dh, const void* gate_up, int64_t rows, int64_t F, int32_t E, const void* out,
+                                  const float* row_amax, const float* col_amax) {
+  if (rows < 0 || F < 0 || E < 0 || F % 16 != 0) return NVFP4_ERR_INVALID_ARG;
+  if (rows > 0 && F > 0 && (dh == nullptr || gate_up == nullptr || out == nullptr)) return NVFP4_ERR_INVALID_ARG;
+  // 8 CTAs of 32 chunks of 256 columns
+  if (E > NVFP4_MAX_GROUPS || rows > kMaxRows || F > 8 * 32 * kBwChunk) return NVFP4_ERR_UNSUPPORTED;
+  if (!aligned(dh, 16) || !aligned(gate_up, 16) || !aligned(out, 16) || !aligned(row_amax, 4) || !aligned(col_amax, 4))
+    return NVFP4_ERR_UNSUPPORTED;
+  return NVFP4_OK;
+}
+
+struct ShrinkArgs {
+  const uint16_t *x, *A;
+  const float* factor;
+  const int32_t* ids;
+  float* u;
+  int32_t* status;
+  int32_t rows, K, adapters;
+};
+
+template <int kMT, int kNT>
+nvfp4_status launch_shrink(const ShrinkArgs& s, int sms, cudaStream_t stream) {
+  constexpr int kTok = 16 * kMT;
+  const int64_t blocks = (s.rows + kTok - 1) / kTok;
+  // adapters side by side and K over a cluster while that fills the GPU
+  int slots = 1, cn = 1;
+  while (slots < kTok && slots < s.adapters && blocks * slots < sms) slots *= 2;
+  while (cn < 8 && blocks * slots * cn < 2 * sms && (s.K + 31) / 32 >= 16 * cn) cn *= 2;
+  auto kernel = adapter_shrink_kernel<kMT, kNT>;
+  const size_t smem = static_cast<size_t>(8) * kTok * 8 * kNT * 4;
+  if (smem > 46 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return NVFP4_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks * cn), static_cast<unsigned>(slots));
+  cfg.blockDim = dim3(kAdThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cn);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, s.x, s.A, s.factor, s.ids, s.u, s.status, s.rows, s.K, s.adapters,
+                                        static_cast<int32_t>(cn), static_cast<int32_t>(slots)));
+}
+
+template <int kMT>
+nvfp4_status launch_shrink_rank(const ShrinkArgs& s, int rank, int sms, cudaStream_t stream) {
+  switch (rank / 8) {
+    case 1: return launch_shrink<kMT, 1>(s, sms, stream);
+    case 2: return launch_shrink<kMT, 2>(s, sms, stream);
+    case 3: return launch_shrink<kMT, 3>(s, sms, stream);
+    case 4: return launch_shrink<kMT, 4>(s, sms, stream);
+    case 5: return launch_shrink<kMT, 5>(s, sms, stream);
+    case 6: return launch_shrink<kMT, 6>(s, sms, stream);
+    case 7: return launch_shrink<kMT, 7>(s, sms, stream);
+    default: return launch_shrink<kMT, 8>(s, sms, stream);
+  }
 }
 
 }  // namespace
@@ -1064,6 +1198,93 @@ nvfp4_status nvfp4_group_wgrad_graphsafe(const nvfp4_matrix* dy, const nvfp4_mat
   s = cuda_status(cudaMemsetAsync(status_dev, 0, sizeof(int32_t), stream));
   if (s != NVFP4_OK || N == 0 || num_groups == 0) return s;
   return launch_gemm<kGemmWgrad>(routing, a, capacity_rows, num_groups * K, num_groups * N, stream);
+}
+
+nvfp4_status nvfp4_group_gated_backward(const void* dh_bf16, const void* gate_up_bf16, int64_t sum_M, int64_t F,
+                                        const int64_t* m_splits_host, int32_t num_groups, void* d_gate_up_bf16,
+                                        float* row_amax, float* col_amax, cudaStream_t stream) {
+  nvfp4_status s = check_gated_backward(dh_bf16, gate_up_bf16, sum_M, F, num_groups, d_gate_up_bf16, row_amax, col_amax);
+  if (s != NVFP4_OK) return s;
+  static thread_local HostRouting routing;
+  s = host_routing(m_splits_host, num_groups, sum_M, routing);
+  if (s != NVFP4_OK || F == 0) return s;
+  return launch_gated_backward(routing, dh_bf16, gate_up_bf16, sum_M, F, d_gate_up_bf16, row_amax, col_amax, stream);
+}
+
+nvfp4_status nvfp4_group_gated_backward_graphsafe(const void* dh_bf16, const void* gate_up_bf16, int64_t capacity_rows,
+                                                  int64_t F, const int64_t* first_dims_dev,
+                                                  const int64_t* tensor_offsets_dev, int32_t num_groups,
+                                                  void* d_gate_up_bf16, float* row_amax, float* col_amax,
+                                                  int32_t* status_dev, cudaStream_t stream) {
+  nvfp4_status s =
+      check_gated_backward(dh_bf16, gate_up_bf16, capacity_rows, F, num_groups, d_gate_up_bf16, row_amax, col_amax);
+  if (s != NVFP4_OK) return s;
+  if (F == 0) return NVFP4_ERR_INVALID_ARG;
+  DeviceRouting routing;
+  s = device_routing(first_dims_dev, tensor_offsets_dev, status_dev, 2 * F, capacity_rows, num_groups, kBlockRows,
+                     routing);
+  if (s != NVFP4_OK) return s;
+  s = cuda_status(cudaMemsetAsync(status_dev, 0, sizeof(int32_t), stream));
+  if (s != NVFP4_OK) return s;
+  return launch_gated_backward(routing, dh_bf16, gate_up_bf16, capacity_rows, F, d_gate_up_bf16, row_amax, col_amax,
+                               stream);
+}
+
+size_t nvfp4_adapter_workspace_bytes(int64_t rows, int32_t rank) {
+  if (rows < 0 || rank < 0 || rank > kAdMaxRank || rows > kMaxRows) return 0;
+  return static_cast<size_t>(rows) * rank * sizeof(float);
+}
+
+nvfp4_status nvfp4_adapter_gemm(const void* x_bf16, const nvfp4_matrix* x, int64_t rows, int64_t K, const nvfp4_matrix* w,
+                                int64_t N, const void* a_bf16, const void* b_bf16, const float* factor,
+                                int32_t num_adapters, int32_t rank, const int32_t* ids_dev, void* y, int32_t y_dtype,
+                                void* workspace, size_t workspace_bytes, int32_t* status_dev, cudaStream_t stream) {
+  if (!out_dtype_ok(y_dtype) || num_adapters < 0 || rank < 8 || rank % 8 != 0 || status_dev == nullptr)
+    return NVFP4_ERR_INVALID_ARG;
+  nvfp4_status s = check_gemm(x, rows, K, 1, w, N, N, y);
+  if (s != NVFP4_OK) return s;
+  if (rows > 0 && (ids_dev == nullptr || (K > 0 && x_bf16 == nullptr) || workspace == nullptr ||
+                   workspace_bytes < nvfp4_adapter_workspace_bytes(rows, rank)))
+    return NVFP4_ERR_INVALID_ARG;
+  if (num_adapters > 0 && (factor == nullptr || (K > 0 && a_bf16 == nullptr) || (N > 0 && b_bf16 == nullptr)))
+    return NVFP4_ERR_INVALID_ARG;
+  if (rank > kAdMaxRank || (x->scale_layout == NVFP4_SCALE_TILED_128X4 && rows % kRows != 0)) return NVFP4_ERR_UNSUPPORTED;
+  if (!aligned(x_bf16, 16) || !aligned(a_bf16, 16) || !aligned(b_bf16, 16) || !aligned(workspace, 16) ||
+      !aligned(factor, 4) || !aligned(ids_dev, 4) || !aligned(status_dev, 4))
+    return NVFP4_ERR_UNSUPPORTED;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return NVFP4_ERR_CUDA;
+  s = cuda_status(cudaMemsetAsync(status_dev, 0, sizeof(int32_t), stream));
+  if (s != NVFP4_OK || rows == 0 || N == 0) return s;
+  float* u = static_cast<float*>(workspace);
+  NVFP4_SPANS(SpanList{}
+                  .add(x_bf16, 2 * static_cast<size_t>(rows) * K, false)
+                  .add(a_bf16, 2 * static_cast<size_t>(num_adapters) * rank * K, false)
+                  .add(factor, 4 * static_cast<size_t>(num_adapters), false)
+                  .add(ids_dev, 4 * static_cast<size_t>(rows), false)
+                  .add(u, nvfp4_adapter_workspace_bytes(rows, rank), true)
+                  .add(status_dev, 4, true)
+                  .set(stream));
+  const ShrinkArgs sh{static_cast<const uint16_t*>(x_bf16), static_cast<const uint16_t*>(a_bf16), factor, ids_dev, u,
+                      status_dev, static_cast<int32_t>(rows), static_cast<int32_t>(K), num_adapters};
+  // 32-row blocks halve the reads of A once there are blocks for every SM
+  s = rows >= 32 * static_cast<int64_t>(sms) ? launch_shrink_rank<2>(sh, rank, sms, stream)
+                                             : launch_shrink_rank<1>(sh, rank, sms, stream);
+  if (s != NVFP4_OK) return s;
+  static thread_local HostRouting routing;
+  const int64_t one[1] = {rows};
+  s = host_routing(one, 1, rows, routing, 1);
+  if (s != NVFP4_OK) return s;
+  GemmArgs a = gemm_args(x, K, w, N, y, y_dtype == NVFP4_OUT_F32);
+  a.u = u;
+  a.ids = ids_dev;
+  a.b = static_cast<const uint16_t*>(b_bf16);
+  a.rank = rank;
+  a.adapters = num_adapters;
+  a.status = status_dev;
+  return launch_gemm<kGemmAdapter>(routing, a, rows, N, rows, stream);
 }
 
 nvfp4_status nvfp4_mx_group_cast(const void* x_bf16, int64_t sum_M, int64_t K, const int64_t* m_splits_host,

@@ -1,0 +1,167 @@
+"""Low-rank adapters beside a shared NVFP4 projection against fp64."""
+import pytest
+import torch
+
+from nvfp4_row_scaled_b200 import abi
+
+from .products import COMPACT, TILED, check, product, random_matrix
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def cuda_ready():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from nvfp4_row_scaled_b200.build import build_library
+    build_library()
+    abi.lib()
+
+
+def case(rows, K, N, R, L, ids, seed, layout=COMPACT):
+    g = torch.Generator().manual_seed(seed)
+    x, xv = random_matrix(rows, K, seed, layout)
+    w, wv = random_matrix(N, K, seed + 1, layout)
+    x["s2"] *= 2.0 ** -6
+    xv = xv * 2.0 ** -6
+    xb = torch.randn(rows, K, generator=g).to(torch.bfloat16)
+    a = (torch.randn(L, R, K, generator=g) * K ** -0.5).to(torch.bfloat16)
+    b = torch.randn(L, N, R, generator=g).to(torch.bfloat16)
+    f = torch.rand(L, generator=g) * 2
+    return dict(x=x, xv=xv, w=w, wv=wv, xb=xb.cuda(), a=a.cuda(), b=b.cuda(), f=f.cuda(),
+                ids=torch.tensor(ids, dtype=torch.int32).cuda())
+
+
+def reference(c):
+    """fp64, and the bound: the projection's; K roundings of 2^-24 in u's fp32
+    sums (truncated MMA steps of 16: at most K / 4 cuts of 2^-23), R + 2 in
+    the second sum and one in the last addition."""
+    p, lim = product(c["xv"], c["wv"])
+    xb, a, b, f = (c[k].double().cpu() for k in ("xb", "a", "b", "f"))
+    K, R, L = xb.shape[1], a.shape[1], a.shape[0]
+    for t, i in enumerate(c["ids"].cpu().tolist()):
+        if 0 <= i < L:
+            u = f[i] * (a[i] @ xb[t])
+            lu = (K / 4 + 4) * 2.0 ** -23 * f[i] * (a[i].abs() @ xb[t].abs())
+            y = b[i] @ u
+            s = b[i].abs() @ u.abs()
+            lim[t] += b[i].abs() @ lu + (R + 3) * 2.0 ** -24 * (s + p[t].abs())
+            p[t] += y
+    return p, lim
+
+
+def run(c, dtype=torch.bfloat16, extra=2):
+    rows, N, R = c["xb"].shape[0], c["b"].shape[1], c["a"].shape[1]
+    buf = torch.full((rows + extra, N), 7.0, dtype=dtype, device="cuda")
+    ws = abi.alloc_adapter_workspace(rows, R)
+    ws.fill_(0xFF)  # NaN: what the second half reads has to be written by the first
+    st = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    abi.nvfp4_adapter_gemm(c["xb"], c["x"], c["w"], c["a"], c["b"], c["f"], c["ids"], buf[:rows], ws, st)
+    assert bool((buf[rows:] == 7.0).all())
+    return buf[:rows], int(st.item())
+
+
+def spread(rows, L, kind):
+    if kind == "one":
+        return [L - 1] * rows
+    if kind == "each":
+        return [i % L for i in range(rows)]
+    if kind == "runs":
+        return [(i // 37) % (L + 1) - 1 for i in range(rows)]
+    if kind == "none":
+        return [-1] * rows
+    return [(i * 7919) % (L + 1) - 1 for i in range(rows)]
+
+
+@pytest.mark.parametrize("kind", ["one", "each", "runs", "none", "mixed"])
+@pytest.mark.parametrize("rows,K,N,R,L", [(1, 64, 16, 8, 1), (17, 256, 144, 16, 5), (64, 1024, 256, 24, 64), (300, 528, 272, 64, 9),
+                                          (33, 4096, 128, 40, 3)])
+def test_adapters(rows, K, N, R, L, kind):
+    c = case(rows, K, N, R, L, spread(rows, L, kind), rows + K)
+    y, st = run(c)
+    assert st == 0
+    check(y, *reference(c), f"{rows} {K} {N} {R} {L} {kind}")
+
+
+@pytest.mark.parametrize("R", [8, 32, 48, 56, 64])
+def test_fp32_and_every_rank(R):
+    c = case(40, 320, 48, R, 4, spread(40, 4, "mixed"), R)
+    y, st = run(c, torch.float32)
+    assert st == 0
+    check(y, *reference(c), f"rank {R}")
+
+
+def test_prompts_of_many_rows():
+    """More than 32 rows a SM: the wider token blocks."""
+    rows = 148 * 32 + 5
+    c = case(rows, 128, 64, 16, 6, [(i // 611) % 7 - 1 for i in range(rows)], 3)
+    y, st = run(c)
+    assert st == 0
+    check(y, *reference(c))
+
+
+def test_tiled_operands():
+    c = case(256, 256, 256, 16, 3, spread(256, 3, "runs"), 4, TILED)
+    y, st = run(c)
+    assert st == 0
+    check(y, *reference(c))
+
+
+def test_ids_outside_the_adapters():
+    """Reported, and such a token gets no adapter."""
+    ids = [0, 5, -2, 1, 2 ** 31 - 1, -2 ** 31, 2, -1]
+    c = case(8, 128, 48, 8, 3, ids, 5)
+    y, st = run(c)
+    assert st == abi.NVFP4_ERR_ROUTING
+    check(y, *reference(c))
+
+
+def test_no_adapter_equals_the_projection():
+    c = case(50, 256, 160, 16, 2, [-1] * 50, 6)
+    y, st = run(c, torch.float32)
+    z = torch.empty_like(y)
+    abi.nvfp4_group_gemm(c["x"], [50], c["w"], z)
+    assert st == 0 and torch.equal(y, z)
+
+
+def test_no_adapters_at_all():
+    c = case(9, 64, 16, 8, 1, [-1] * 9, 7)
+    c["a"], c["b"], c["f"] = c["a"][:0], c["b"][:0], c["f"][:0]
+    y, st = run(c)
+    assert st == 0
+    check(y, *product(c["xv"], c["wv"]))
+
+
+def test_token_does_not_depend_on_its_neighbours():
+    """The same bits alone and among others, whatever they use."""
+    c = case(70, 512, 96, 16, 8, spread(70, 8, "each"), 8)
+    y, _ = run(c, torch.float32)
+    for t in (0, 13, 69):
+        one = dict(c, xb=c["xb"][t:t + 1].contiguous(), ids=c["ids"][t:t + 1].contiguous(),
+                   x=abi.matrix(*(c["x"][k][t:t + 1].contiguous() for k in ("data", "scale", "s2"))))
+        z, _ = run(one, torch.float32)
+        assert torch.equal(y[t:t + 1], z)
+    again, _ = run(c, torch.float32)
+    assert torch.equal(y, again)
+
+
+def test_graph_replays_with_other_ids():
+    c = case(20, 256, 64, 16, 4, spread(20, 4, "each"), 9)
+    y = torch.empty(20, 64, device="cuda")
+    ws = abi.alloc_adapter_workspace(20, 16)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call():
+        abi.nvfp4_adapter_gemm(c["xb"], c["x"], c["w"], c["a"], c["b"], c["f"], c["ids"], y, ws, st)
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for kind in ("one", "none", "mixed"):
+        c["ids"].copy_(torch.tensor(spread(20, 4, kind), dtype=torch.int32))
+        ws.fill_(0xFF)
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0
+        check(y, *reference(c), kind)

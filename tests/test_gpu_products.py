@@ -1,5 +1,7 @@
 """Grouped products of NVFP4 casts against fp64: nvfp4_group_gemm,
 nvfp4_group_gated_gemm and nvfp4_group_wgrad, host-split and graph-safe."""
+import os
+
 import pytest
 import torch
 
@@ -141,3 +143,186 @@ def run_wgrad(m, N, K, dtype, dl, xl):
         want, lim = product(dv[g], xv[g])
         check(dw[g], want, lim, f"group {g}")
     assert bool((buf[E * N * K:] == 7.0).all())
+
+
+# ----------------------------------------------------------------- routing
+
+def routings(m, K, rows):
+    fd, offs = abi.routing_tensors(m, K)
+    return fd, offs, torch.full((1,), -1, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("m,cap", [([3, 0, 70, 300], 400), ([0, 0, 0], 64), ([128, 128], 256)])
+def test_graphsafe_equals_host_split(m, cap):
+    """The same bits for the same routing; rows behind the routed total stay."""
+    K, N, E, rows = 512, 144, len(m), sum(m)
+    x, _ = random_matrix(cap, K, 7)
+    w, _ = random_matrix(E * 2 * N, K, 8)
+    w1 = abi.matrix(w["data"][:E * N].contiguous(), w["scale"][:E * N].contiguous(), w["s2"][:E * N].contiguous())
+    xr = abi.matrix(x["data"][:rows].contiguous(), x["scale"][:rows].contiguous(), x["s2"][:rows].contiguous())
+    fd, offs, st = routings(m, K, rows)
+    y = torch.full((cap, N), 7.0, device="cuda")
+    yh = torch.empty(rows, N, device="cuda")
+    abi.nvfp4_group_gemm_graphsafe(x, fd, offs, w1, y, st)
+    abi.nvfp4_group_gemm(xr, m, w1, yh)
+    assert int(st.item()) == 0
+    assert torch.equal(y[:rows], yh) and bool((y[rows:] == 7.0).all())
+    h = torch.full((cap, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    p = torch.full((cap, 2 * N), 7.0, dtype=torch.bfloat16, device="cuda")
+    hh, ph = h[:rows].clone(), p[:rows].clone()
+    abi.nvfp4_group_gated_gemm_graphsafe(x, fd, offs, w, h, st, gate_up=p)
+    abi.nvfp4_group_gated_gemm(xr, m, w, hh, gate_up=ph)
+    assert int(st.item()) == 0
+    assert torch.equal(h[:rows], hh) and torch.equal(p[:rows], ph)
+    assert bool((h[rows:] == 7.0).all()) and bool((p[rows:] == 7.0).all())
+
+
+@pytest.mark.parametrize("fault", ["offset", "first", "beyond"])
+def test_graphsafe_bad_routing_writes_nothing(fault):
+    K, N = 128, 32
+    x, _ = random_matrix(64, K, 9)
+    w, _ = random_matrix(2 * 2 * N, K, 10)
+    w1 = abi.matrix(w["data"][:2 * N].contiguous(), w["scale"][:2 * N].contiguous(), w["s2"][:2 * N].contiguous())
+    fd, offs, st = routings([32, 32], K, 64)
+    if fault == "offset":
+        offs[1] += 1
+    elif fault == "first":
+        fd[0] = 16
+    else:
+        fd[1], offs[2] = 48, 80 * K
+    y = torch.full((64, N), 7.0, device="cuda")
+    abi.nvfp4_group_gemm_graphsafe(x, fd, offs, w1, y, st)
+    assert int(st.item()) == abi.NVFP4_ERR_ROUTING and bool((y == 7.0).all())
+    h = torch.full((64, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    abi.nvfp4_group_gated_gemm_graphsafe(x, fd, offs, w, h, st)
+    assert int(st.item()) == abi.NVFP4_ERR_ROUTING and bool((h == 7.0).all())
+
+
+def test_graphsafe_tiled_rows_need_128():
+    x, _ = random_matrix(256, 128, 11, TILED)
+    w, _ = random_matrix(2 * 128, 128, 12, TILED)
+    fd, offs, st = routings([64, 192], 128, 256)
+    y = torch.full((256, 128), 7.0, device="cuda")
+    abi.nvfp4_group_gemm_graphsafe(x, fd, offs, w, y, st)
+    assert int(st.item()) == abi.NVFP4_ERR_UNSUPPORTED and bool((y == 7.0).all())
+
+
+def test_uniform_groups():
+    x, xv = random_matrix(96, 64, 13)
+    w, wv = random_matrix(3 * 48, 64, 14)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = torch.empty(96, 48, device="cuda")
+    abi.nvfp4_group_gemm_graphsafe(x, None, None, w, y, st, num_groups=3)
+    assert int(st.item()) == 0
+    check(y, *stacked([32] * 3, xv, wv, 48))
+
+
+def test_wgrad_graphsafe_equals_host_split():
+    m, N, K = [48, 0, 160], 144, 80
+    dy, _ = random_columns(m, N, 300, COMPACT)
+    x, _ = random_columns(m, K, 400, COMPACT)
+    fd, offs, st = routings(m, K, sum(m))
+    a, b = torch.full((3, N, K), 7.0, device="cuda"), torch.empty(3, N, K, device="cuda")
+    abi.nvfp4_group_wgrad_graphsafe(dy, x, sum(m), fd, offs, a, st)
+    abi.nvfp4_group_wgrad(dy, x, m, b)
+    assert int(st.item()) == 0 and torch.equal(a, b) and bool((a[1] == 0).all())
+    fd[0], offs[1] = 40, 40 * K  # not a multiple of 16 rows
+    a.fill_(7.0)
+    fd[2], offs[3] = 168, 208 * K
+    abi.nvfp4_group_wgrad_graphsafe(dy, x, sum(m), fd, offs, a, st)
+    assert int(st.item()) != 0
+    fd[2] = 168
+    offs[2] = 40 * K
+    abi.nvfp4_group_wgrad_graphsafe(dy, x, sum(m), fd, offs, a, st)
+    assert int(st.item()) in (abi.NVFP4_ERR_UNSUPPORTED, abi.NVFP4_ERR_ROUTING) and bool((a == 7.0).all())
+
+
+def test_graph_replays_with_other_routings():
+    """One captured graph, the routing rewritten between replays."""
+    K, N, E, cap = 256, 64, 4, 200
+    x, xv = random_matrix(cap, K, 15)
+    w, wv = random_matrix(E * N, K, 16)
+    fd, offs, st = routings([50] * 4, K, cap)
+    y = torch.empty(cap, N, device="cuda")
+    abi.nvfp4_group_gemm_graphsafe(x, fd, offs, w, y, st)  # before the capture
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        abi.nvfp4_group_gemm_graphsafe(x, fd, offs, w, y, st)
+    for m in ([200, 0, 0, 0], [1, 2, 3, 4], [0, 99, 0, 101], [0, 0, 0, 0]):
+        f2, o2 = abi.routing_tensors(m, K)
+        fd.copy_(f2)
+        offs.copy_(o2)
+        y.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0
+        n = sum(m)
+        if n:
+            check(y[:n], *stacked(m, xv, wv, N), str(m))
+        assert bool((y[n:] == 7.0).all())
+
+
+def test_zero_contraction_gives_zeros():
+    x, _ = random_matrix(5, 0, 17)
+    w, _ = random_matrix(2 * 32, 0, 18)
+    y = torch.full((5, 32), 7.0, device="cuda")
+    abi.nvfp4_group_gemm(x, [5, 0], w, y)
+    assert bool((y == 0).all())
+
+
+def test_nan_scale_stays_in_its_rows():
+    """A NaN block scale of one token or one weight row reaches that row and column only."""
+    x, xv = random_matrix(300, 256, 19)
+    w, wv = random_matrix(160, 256, 20)
+    x["scale"][17, 3] = 0x7F
+    w["scale"][130, 1] = 0x7F
+    y = torch.empty(300, 160, device="cuda")
+    abi.nvfp4_group_gemm(x, [300], w, y)
+    nan = torch.isnan(y.cpu())
+    want = torch.zeros(300, 160, dtype=torch.bool)
+    want[17], want[:, 130] = True, True
+    assert torch.equal(nan, want)
+    p, b = product(xv, wv)
+    keep = ~want
+    check(y.cpu()[keep], p[keep], b[keep])
+
+
+def test_two_streams_at_once():
+    """Calls on two streams share nothing."""
+    if os.environ.get("NVFP4RS_LIBRARY"):
+        pytest.skip("the bounds-checked build keeps one table of ranges: one call at a time")
+    K, N = 1024, 256
+    ins = [(random_matrix(200, K, 21 + i), random_matrix(N, K, 31 + i)) for i in range(2)]
+    ys = [torch.empty(200, N, device="cuda") for _ in range(2)]
+    ss = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i in range(2):
+            abi.nvfp4_group_gemm(ins[i][0][0], [200], ins[i][1][0], ys[i], stream=ss[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        check(ys[i], *product(ins[i][0][1], ins[i][1][1]), f"stream {i}")
+
+
+def test_offsets_past_32_bits():
+    """The last rows of an output of more than 2^31 elements, and of weights of
+    more than 2^32 codes."""
+    K, N, rows = 32, 16400, 131200
+    x, xv = random_matrix(64, K, 22)
+    big = abi.matrix(*(torch.cat([torch.zeros(rows - 64, *x[k].shape[1:], dtype=x[k].dtype, device="cuda"), x[k]])
+                       for k in ("data", "scale", "s2")))
+    w, wv = random_matrix(N, K, 23)
+    y = torch.empty(rows, N, dtype=torch.bfloat16, device="cuda")
+    abi.nvfp4_group_gemm(big, [rows], w, y)
+    check(y[-64:], *product(xv, wv))
+    assert bool((y[:64] == 0).all())
+    del y, big
+    E, N, K = 70, 16384, 4096
+    wl, wlv = random_matrix(N, K, 24)
+    rep = abi.matrix(*(torch.cat([torch.zeros((E - 1) * N, *wl[k].shape[1:], dtype=wl[k].dtype, device="cuda"), wl[k]])
+                       for k in ("data", "scale", "s2")))
+    x, xv = random_matrix(5, K, 25)
+    y = torch.empty(5, N, device="cuda")
+    abi.nvfp4_group_gemm(x, [0] * (E - 1) + [5], rep, y)
+    check(y, *product(xv, wlv))
