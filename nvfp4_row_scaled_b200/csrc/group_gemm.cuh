@@ -69,7 +69,8 @@ constexpr int kGI = 128;             // I rows (accumulator lanes) of a tile
 constexpr int kGJ = 256;             // most J rows (accumulator columns) of a tile
 constexpr int kGK = 256;             // contraction elements of a stage: 128 bytes a row
 constexpr int kGStages = 4;
-constexpr int kGBoxJ = 32;           // J rows of one TMA box
+constexpr int kGBigJ = 128;          // J rows of a TMA box ...
+constexpr int kGBoxJ = 32;           // ... and of one in a tile's rest
 constexpr int kGIBytes = kGI * 128;
 constexpr int kGJBytes = kGJ * 128;
 constexpr int kGScaleTile = 512;     // 128 rows x 4 scales
@@ -149,6 +150,12 @@ __device__ __forceinline__ void mma_nvf4(uint32_t d, uint64_t a, uint64_t b, uin
       "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(static_cast<uint32_t>(accumulate))
       : "memory");
+}
+// true in one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
@@ -350,12 +357,50 @@ __device__ __forceinline__ void add_adapters(float (&y)[32], const GemmArgs& a, 
     y[k] = __uint_as_float(static_cast<uint32_t>(acc[k])) + __uint_as_float(static_cast<uint32_t>(acc[k] >> 32));
 }
 
+// One stage's scale copies and MMAs, by one thread. All descriptors are one
+// base plus constants and the full stage is unrolled: an operand built per
+// instruction costs about 70 cycles of issue for each copy or MMA, more than the
+// 128 cycles an N = 256 MMA runs (measured: 12 copies and 4 MMAs 1070 cycles
+// a stage so, 513 as here, which is the MMAs alone).
+template <bool kGated, bool kFull>
+__device__ __forceinline__ void issue_stage(uint32_t st, uint32_t tmem, uint32_t acc, uint32_t idesc, int ksteps,
+                                            bool two, bool first) {
+  constexpr int kIData = kGated ? 2 * kGIBytes : kGIBytes;
+  constexpr int kISf = (kGated ? 2 : 1) * 4 * kGScaleTile;
+  constexpr int kTileUnits = kGScaleTile >> 4;
+  constexpr int kJCols = kGated ? 4 : 8;
+  const uint64_t di = mma_desc(st), dj = mma_desc(st + kIData);
+  const uint64_t si = scale_desc(st + kGDataBytes), sj = scale_desc(st + kGDataBytes + kISf);
+  const uint32_t ti = tmem + kGSfCol, tj = ti + (kGated ? 32 : 16);
+#pragma unroll
+  for (int k = 0; k < 4; k++)
+    if (kFull || k < ksteps) {
+      tmem_copy_scales(ti + 4 * k, si + kTileUnits * k);
+      if (kGated) tmem_copy_scales(ti + 16 + 4 * k, si + kTileUnits * (4 + k));
+      tmem_copy_scales(tj + kJCols * k, sj + kTileUnits * k);
+    }
+  if (!kGated && two) {
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+      if (kFull || k < ksteps) tmem_copy_scales(tj + 8 * k + 4, sj + kTileUnits * (4 + k));
+  }
+#pragma unroll
+  for (int k = 0; k < 4; k++)
+    if (kFull || k < ksteps) {
+      mma_nvf4(acc, di + 2 * k, dj + 2 * k, idesc, ti + 4 * k, tj + kJCols * k, !first || k > 0);
+      if (kGated)
+        mma_nvf4(acc + 128, di + (kGIBytes >> 4) + 2 * k, dj + 2 * k, idesc, ti + 16 + 4 * k, tj + kJCols * k,
+                 !first || k > 0);
+    }
+}
+
 // ------------------------------------------------------------------ kernel
 
 template <class Routing, int kMode, bool kTma>
 __global__ void __launch_bounds__(kGThreads, 1)
 group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant__ CUtensorMap imap,
-                  const __grid_constant__ CUtensorMap jmap, const __grid_constant__ GemmArgs a) {
+                  const __grid_constant__ CUtensorMap jmap, const __grid_constant__ CUtensorMap jmap_small,
+                  const __grid_constant__ GemmArgs a) {
   constexpr bool kGated = kMode == kGemmGated;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -390,115 +435,111 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
 
   if (sm.routing.ok) {
     if (warp == 0 && a.producer) {
-      if (lane == 0) {
-        GemmWalk<kMode> walk(sm.routing, a);
-        GemmTile t;
-        uint32_t n = 0;
-        bool ok = true;
-        for (int64_t ti = blockIdx.x; ok && walk.seek(ti, t); ti += gridDim.x) {
-          const int nkb = (t.kc + kGK - 1) / kGK;
-          const int boxes = (t.jv + kGBoxJ - 1) / kGBoxJ;
-          for (int kb = 0; kb < nkb; kb++, n++) {
-            const int s = n % kGStages;
-            if (!mbar_wait(&sm.empty[s], ((n / kGStages) & 1) ^ 1)) {
-              ok = false;
-              break;
-            }
-            uint8_t* st = sm.stage[s];
-            const int ksteps = min(4, (t.kc - kb * kGK + 63) / 64);
-            const int jblocks = (t.jv + 127) / 128;
-            uint32_t bytes = 0;
-            if (kTma) bytes += (kGated ? 2 : 1) * kGIBytes + boxes * kGBoxJ * 128;
-            if (a.i.tiled) bytes += (kGated ? 2 : 1) * ksteps * kGScaleTile;
-            if (a.j.tiled) bytes += jblocks * ksteps * kGScaleTile;
-            mbar_expect_tx(&sm.full[s], bytes);
-            const uint64_t pol = policy_evict_normal();
-            if (kTma) {
-              tma_load_2d(st, &imap, kb * 128, static_cast<int>(t.irow), &sm.full[s], pol);
-              if (kGated) tma_load_2d(st + kGIBytes, &imap, kb * 128, static_cast<int>(t.irow + a.ni), &sm.full[s], pol);
-              for (int b = 0; b < boxes; b++)
-                tma_load_2d(st + kIData + b * kGBoxJ * 128, &jmap, kb * 128, static_cast<int>(t.jrow) + b * kGBoxJ,
-                            &sm.full[s], pol);
-            }
-            // tiled scales: tile (row block, k step) at (block * kc/64 + step) * 512
-            uint8_t* sf = st + kGDataBytes;
-            const int64_t kt = t.kc / 64;
-            if (a.i.tiled) {
-              const uint8_t* src = a.i.scale + (kMode == kGemmWgrad ? t.goff * a.ni / 16 + t.i0 / 128 * kt * kGScaleTile
-                                                                    : t.irow / 128 * kt * kGScaleTile) +
-                                   kb * 4 * kGScaleTile;
-              bulk_load(sf, src, ksteps * kGScaleTile, &sm.full[s]);
-              if (kGated) bulk_load(sf + 4 * kGScaleTile, src + a.ni / 128 * kt * kGScaleTile, ksteps * kGScaleTile, &sm.full[s]);
-            }
-            if (a.j.tiled) {
-              const uint8_t* src = a.j.scale + (kMode == kGemmWgrad ? t.goff * a.nj / 16 + t.j0 / 128 * kt * kGScaleTile
-                                                                    : t.jrow / 128 * kt * kGScaleTile) +
-                                   kb * 4 * kGScaleTile;
-              for (int b = 0; b < jblocks; b++)
-                bulk_load(sf + kISf + b * 4 * kGScaleTile, src + b * kt * kGScaleTile, ksteps * kGScaleTile, &sm.full[s]);
-            }
+      GemmWalk<kMode> walk(sm.routing, a);
+      GemmTile t;
+      const bool elected = elect_one();
+      uint32_t n = 0;
+      bool ok = true;
+      const uint64_t pol = policy_evict_normal();
+      for (int64_t ti = blockIdx.x; ok && walk.seek(ti, t); ti += gridDim.x) {
+        const int nkb = (t.kc + kGK - 1) / kGK;
+        // J rows: boxes of 128, the rest in boxes of 32
+        const int big = t.jv / kGBigJ, small = (t.jv - big * kGBigJ + kGBoxJ - 1) / kGBoxJ;
+        const int jblocks = (t.jv + 127) / 128;
+        const int64_t kt = t.kc / 64;
+        // tiled scales: tile (row block, k step) at (block * kc/64 + step) * 512
+        const uint8_t* is = a.i.scale + (kMode == kGemmWgrad ? t.goff * a.ni / 16 + t.i0 / 128 * kt * kGScaleTile
+                                                             : t.irow / 128 * kt * kGScaleTile);
+        const uint8_t* js = a.j.scale + (kMode == kGemmWgrad ? t.goff * a.nj / 16 + t.j0 / 128 * kt * kGScaleTile
+                                                             : t.jrow / 128 * kt * kGScaleTile);
+        const int iy = static_cast<int>(t.irow), jy = static_cast<int>(t.jrow);
+        uint32_t data_bytes = 0, tiles = 0;
+        if (kTma) data_bytes = (kGated ? 2 : 1) * kGIBytes + (big * kGBigJ + small * kGBoxJ) * 128;
+        if (a.i.tiled) tiles += kGated ? 2 : 1;
+        if (a.j.tiled) tiles += jblocks;
+        for (int kb = 0; kb < nkb; kb++, n++) {
+          const int s = n % kGStages;
+          if (!mbar_wait(&sm.empty[s], ((n / kGStages) & 1) ^ 1)) {
+            ok = false;
+            break;
           }
-        }
-        if (!ok) {
-          sm.gave_up = 1;
-          for (uint32_t k = n > kGStages ? n - kGStages : 0; k < n; k++)
-            mbar_wait(&sm.full[k % kGStages], (k / kGStages) & 1);
+          if (elected) {
+            uint8_t* st = sm.stage[s];
+            uint64_t* bar = &sm.full[s];
+            const uint32_t sf_bytes = min(4, (t.kc - kb * kGK + 63) / 64) * kGScaleTile;
+            mbar_expect_tx(bar, data_bytes + tiles * sf_bytes);
+            if (kTma) {
+              tma_load_2d(st, &imap, kb * 128, iy, bar, pol);
+              if (kGated) tma_load_2d(st + kGIBytes, &imap, kb * 128, iy + a.ni, bar, pol);
+              for (int b = 0; b < big; b++)
+                tma_load_2d(st + kIData + b * kGBigJ * 128, &jmap, kb * 128, jy + b * kGBigJ, bar, pol);
+              for (int b = 0; b < small; b++)
+                tma_load_2d(st + kIData + (big * kGBigJ + b * kGBoxJ) * 128, &jmap_small, kb * 128,
+                            jy + big * kGBigJ + b * kGBoxJ, bar, pol);
+            }
+            uint8_t* sf = st + kGDataBytes;
+            const int32_t so = kb * 4 * kGScaleTile;
+            if (a.i.tiled) {
+              bulk_load(sf, is + so, sf_bytes, bar);
+              if (kGated) bulk_load(sf + 4 * kGScaleTile, is + a.ni / 128 * kt * kGScaleTile + so, sf_bytes, bar);
+            }
+            if (a.j.tiled)
+              for (int b = 0; b < jblocks; b++)
+                bulk_load(sf + kISf + b * 4 * kGScaleTile, js + b * kt * kGScaleTile + so, sf_bytes, bar);
+          }
+          __syncwarp();
         }
       }
+      if (!ok) {
+        sm.gave_up = 1;
+        for (uint32_t k = n > kGStages ? n - kGStages : 0; k < n; k++)
+          mbar_wait(&sm.full[k % kGStages], (k / kGStages) & 1);
+      }
     } else if (warp == 1) {
-      if (lane == 0) {
-        GemmWalk<kMode> walk(sm.routing, a);
-        GemmTile t;
-        uint32_t n = 0, tiles = 0;
-        bool ok = true;
-        for (int64_t ti = blockIdx.x; ok && walk.seek(ti, t); ti += gridDim.x) {
-          const int nkb = (t.kc + kGK - 1) / kGK;
-          if (nkb == 0) continue;
-          if (tiles > 0 && !mbar_wait(&sm.acc_free, (tiles - 1) & 1)) {
+      GemmWalk<kMode> walk(sm.routing, a);
+      GemmTile t;
+      const bool elected = elect_one();
+      uint32_t n = 0, tiles = 0;
+      bool ok = true;
+      const uint32_t stages = smem_addr(sm.stage[0]);
+      for (int64_t ti = blockIdx.x; ok && walk.seek(ti, t); ti += gridDim.x) {
+        const int nkb = (t.kc + kGK - 1) / kGK;
+        if (nkb == 0) continue;
+        if (tiles > 0 && !mbar_wait(&sm.acc_free, (tiles - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t acc = tmem + ((tiles & 1) ? kGAcc1 : 0);
+        const int cols = (t.jv + 15) & ~15;
+        const uint32_t idesc = mma_idesc(cols);
+        for (int kb = 0; kb < nkb; kb++, n++) {
+          const int s = n % kGStages;
+          if (!mbar_wait(&sm.full[s], (n / kGStages) & 1)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t acc = tmem + ((tiles & 1) ? kGAcc1 : 0);
-          const int cols = (t.jv + 15) & ~15;
-          const uint32_t idesc = mma_idesc(cols);
-          const int jblocks = (cols + 127) / 128;
-          const uint32_t sfi = tmem + kGSfCol, sfj = sfi + (kGated ? 32 : 16);
-          for (int kb = 0; kb < nkb; kb++, n++) {
-            const int s = n % kGStages;
-            if (!mbar_wait(&sm.full[s], (n / kGStages) & 1)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const int ksteps = min(4, (t.kc - kb * kGK + 63) / 64);
-            const uint32_t st = smem_addr(sm.stage[s]);
-            const uint32_t sf = st + kGDataBytes;
-            const uint64_t di = mma_desc(st), dj = mma_desc(st + kIData);
-            for (int k = 0; k < ksteps; k++) {
-              tmem_copy_scales(sfi + 4 * k, scale_desc(sf + k * kGScaleTile));
-              if (kGated) tmem_copy_scales(sfi + 16 + 4 * k, scale_desc(sf + (4 + k) * kGScaleTile));
-              tmem_copy_scales(sfj + (kGated ? 4 : 8) * k, scale_desc(sf + kISf + k * kGScaleTile));
-              if (!kGated && jblocks > 1)
-                tmem_copy_scales(sfj + 8 * k + 4, scale_desc(sf + kISf + (4 + k) * kGScaleTile));
-            }
-            for (int k = 0; k < ksteps; k++) {
-              const bool accumulate = kb > 0 || k > 0;
-              mma_nvf4(acc, di + 2 * k, dj + 2 * k, idesc, sfi + 4 * k, sfj + (kGated ? 4 : 8) * k, accumulate);
-              if (kGated)
-                mma_nvf4(acc + 128, di + (kGIBytes >> 4) + 2 * k, dj + 2 * k, idesc, sfi + 16 + 4 * k, sfj + 4 * k,
-                         accumulate);
-            }
+          const int ksteps = min(4, (t.kc - kb * kGK + 63) / 64);
+          if (elected) {
+            const uint32_t st = stages + s * kGStageBytes;
+            if (ksteps == 4)
+              issue_stage<kGated, true>(st, tmem, acc, idesc, 4, cols > 128, kb == 0);
+            else
+              issue_stage<kGated, false>(st, tmem, acc, idesc, ksteps, cols > 128, kb == 0);
             mma_commit(&sm.empty[s]);
           }
-          if (ok) mma_commit(&sm.acc_full);
-          tiles++;
+          __syncwarp();
         }
-        if (!ok) {
-          sm.gave_up = 1;
-          mma_commit(&sm.drain);
-          mbar_wait(&sm.drain, 0);
-        }
+        if (ok && elected) mma_commit(&sm.acc_full);
+        __syncwarp();
+        tiles++;
+      }
+      if (!ok) {
+        sm.gave_up = 1;
+        if (elected) mma_commit(&sm.drain);
+        __syncwarp();
+        mbar_wait(&sm.drain, 0);
       }
     } else if (warp >= kGLoadWarp && warp < kGEpiWarp && a.loaders) {
       const int tid = threadIdx.x - kGLoadWarp * 32;

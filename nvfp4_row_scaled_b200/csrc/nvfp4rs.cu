@@ -660,11 +660,13 @@ nvfp4_status launch_gemm(const Routing& routing, GemmArgs a, int64_t rows, int64
   const bool tma = !kWgrad && a.K % 32 == 0 && a.K > 0;
   a.loaders = !tma || !a.i.tiled || !a.j.tiled;
   a.producer = tma || a.i.tiled || a.j.tiled;
-  CUtensorMap imap, jmap;
+  CUtensorMap imap, jmap, jmap_small;
   std::memset(&imap, 0, sizeof(imap));
   std::memset(&jmap, 0, sizeof(jmap));
+  std::memset(&jmap_small, 0, sizeof(jmap_small));
   if (tma && (!code_tensor_map(&imap, a.i.data, i_rows, a.K, kGI) ||
-              !code_tensor_map(&jmap, a.j.data, j_rows, a.K, kGBoxJ)))
+              !code_tensor_map(&jmap, a.j.data, j_rows, a.K, kGBigJ) ||
+              !code_tensor_map(&jmap_small, a.j.data, j_rows, a.K, kGBoxJ)))
     return NVFP4_ERR_CUDA;
   auto kernel = group_gemm_kernel<Routing, kMode, !kWgrad>;
   if (!tma) kernel = group_gemm_kernel<Routing, kMode, false>;
@@ -706,7 +708,7 @@ nvfp4_status launch_gemm(const Routing& routing, GemmArgs a, int64_t rows, int64
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = kMode == kGemmAdapter ? 1 : 0;
-  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, routing, imap, jmap, a));
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, routing, imap, jmap, jmap_small, a));
 }
 
 GemmOperand operand(const nvfp4_matrix* m) {
