@@ -117,6 +117,7 @@ struct GemmSmem {
   uint32_t tmem;
   uint32_t gave_up;
   RoutingSmem routing;
+  alignas(16) float sj[kGEpiWarps][32];  // the J factors of each epilogue warp's chunk
 };
 
 constexpr size_t gemm_smem_bytes(int E) {
@@ -290,19 +291,63 @@ __device__ __forceinline__ void load_scales(uint8_t* dst, const uint8_t* scale, 
         cp_async<4>(da + k * kGScaleTile, in ? s + 4 * k : scale, in ? 4 : 0);
       }
     } else {
+      // rows start at any byte: the aligned words around the 16 bytes, shifted.
+      // A stacked matrix ends on a 16-byte boundary, so a word that holds a byte
+      // of it lies inside it.
+      const uint32_t sh = (reinterpret_cast<uintptr_t>(s) & 3) * 8;
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(s - (sh >> 3));
+      const int n = cols - first;  // bytes left in the row
+      uint32_t w[5];
+#pragma unroll
+      for (int k = 0; k < 5; k++) w[k] = 4 * k < n + static_cast<int>(sh >> 3) ? gload(p + k) : 0u;
 #pragma unroll
       for (int k = 0; k < 4; k++) {
-        uint32_t w = 0;
-#pragma unroll
-        for (int b = 0; b < 4; b++)
-          if (first + 4 * k + b < cols) w |= static_cast<uint32_t>(gload(s + 4 * k + b)) << (8 * b);
-        *reinterpret_cast<uint32_t*>(d + k * kGScaleTile) = w;
+        uint32_t v = __funnelshift_r(w[k], w[k + 1], sh);
+        const int left = n - 4 * k;
+        if (left < 4) v = left <= 0 ? 0u : v & (0xFFFFFFFFu >> (8 * (4 - left)));
+        *reinterpret_cast<uint32_t*>(d + k * kGScaleTile) = v;
       }
     }
   }
 }
 
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+
+// 32 rows x 32 features of a warp, lane = feature, y[k] = row k: rounded to bf16
+// and stored as 16 bytes (8 features) a lane. Three exchanges between lanes 1,
+// 2 and 4 apart turn columns into rows: after them, register block m of lane l
+// holds row 8 m + (l & 7), features (l & 24) .. + 7, so an instruction writes
+// 64 contiguous bytes of each of 8 rows. Stored one element a lane (2 bytes, 32
+// instructions and their predicates) a 128 x 256 tile took 15 k cycles.
+__device__ __forceinline__ void store_bf16(const float (&y)[32], uint16_t* out, int64_t pitch, int rows, int features,
+                                           int lane) {
+  uint32_t r[16];
+  const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
+#pragma unroll
+  for (int i = 0; i < 16; i++) {
+    const uint32_t p = bf16x2_rn(y[2 * i], y[2 * i + 1]);  // rows 2i (low), 2i + 1
+    const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, p, 1);
+    // even lanes: row 2i of (own, other); odd lanes: row 2i + 1 of (other, own)
+    r[i] = __byte_perm(p, o, b0 ? 0x3276 : 0x5410);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; j++) {  // rows 4j + (lane & 3), four features
+    const uint32_t keep = b1 ? r[2 * j + 1] : r[2 * j], send = b1 ? r[2 * j] : r[2 * j + 1];
+    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, send, 2);
+    r[2 * j] = b1 ? got : keep;
+    r[2 * j + 1] = b1 ? keep : got;
+  }
+#pragma unroll
+  for (int m = 0; m < 4; m++) {  // rows 8m + (lane & 7), eight features
+    const uint32_t k0 = b2 ? r[4 * m + 2] : r[4 * m], k1 = b2 ? r[4 * m + 3] : r[4 * m + 1];
+    const uint32_t s0 = b2 ? r[4 * m] : r[4 * m + 2], s1 = b2 ? r[4 * m + 1] : r[4 * m + 3];
+    const uint32_t g0 = __shfl_xor_sync(0xFFFFFFFFu, s0, 4), g1 = __shfl_xor_sync(0xFFFFFFFFu, s1, 4);
+    const uint4 o = b2 ? make_uint4(g0, g1, k0, k1) : make_uint4(k0, k1, g0, g1);
+    const int row = 8 * m + (lane & 7);
+    if (row < rows && (lane & 24) < features)
+      gstore(reinterpret_cast<uint4*>(out + row * pitch + (lane & 24)), o);
+  }
+}
 
 // The adapters' share of a lane's 32 outputs (feature n of rows row .. row + nc - 1):
 // y[k] += sum_r u[row + k][r] b[id][n][r], in fp32, ranks in order in two
@@ -617,12 +662,24 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
       for (int64_t ti = blockIdx.x; walk.seek(ti, t); ti += gridDim.x) {
         const bool empty = t.kc == 0;
         const int il = 32 * q + lane;
-        const bool live = il < t.iv;
         const int64_t n = t.i0 + il;
+        const bool live = il < t.iv;
         float si = 0.0f, su = 0.0f;
         if (live && !empty) {
           si = gload(&a.i.s2[t.irow + il]);
           if (kGated) su = gload(&a.i.s2[t.irow + a.ni + il]);
+        }
+        const int set = tiles & 1;
+        // chunks of 32 columns; the first one a warp takes holds its part of
+        // the columns both accumulators share (set 0: the last two, set 1: the
+        // first two; gated: of the up or the gate half)
+        constexpr int kChunks = kGated ? 4 : 8;
+        auto chunk = [&](int ci) { return (set == 0 ? (ci == 0 ? kChunks - 2 : 2 * (ci - 1)) : 2 * ci) + half; };
+        float sj[kChunks / 2];
+#pragma unroll
+        for (int ci = 0; ci < kChunks / 2; ci++) {
+          const int c = chunk(ci) * 32 + lane;
+          sj[ci] = c < t.jv && !empty ? gload(&a.j.s2[t.jrow + c]) : 0.0f;
         }
         if (!empty) {
           if (!mbar_wait(&sm.acc_full, tiles & 1)) {
@@ -632,12 +689,8 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
           tc_fence_after();
         }
         if (kMode == kGemmAdapter) grid_dependency_wait();  // u comes from the kernel before this one
-        const int set = tiles & 1;
         const uint32_t acc = tmem + (set ? kGAcc1 : 0) + (static_cast<uint32_t>(32 * q) << 16);
-        // chunks of 32 columns; the first one a warp takes holds its part of
-        // the columns both accumulators share (set 0: the last two, set 1: the
-        // first two; gated: of the up or the gate half)
-        constexpr int kChunks = kGated ? 4 : 8;
+        float* sjw = sm.sj[warp - kGEpiWarp];
         bool freed = empty;
         auto release = [&] {
           if (!freed) {
@@ -647,9 +700,9 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
             freed = true;
           }
         };
+#pragma unroll 1
         for (int ci = 0; ci < kChunks / 2; ci++) {
-          const int c = (set == 0 ? (ci == 0 ? kChunks - 2 : 2 * (ci - 1)) : 2 * ci) + half;
-          const int c0 = c * 32;
+          const int c0 = chunk(ci) * 32;
           if (c0 >= t.jv) {
             if (ci == 0) release();
             continue;
@@ -661,48 +714,51 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
           } else {
             tmem_load32(acc + c0, v);
             if (kGated) tmem_load32(acc + 128 + c0, w);
+            __syncwarp();  // the previous chunk's factors have been read
+            sjw[lane] = ci == 0 ? sj[0] : ci == 1 ? sj[1] : ci == 2 ? sj[kChunks / 2 > 2 ? 2 : 0] : sj[kChunks / 2 - 1];
+            __syncwarp();
             tmem_load_wait(v);
             if (kGated) tmem_load_wait(w);
           }
           if (ci == 0) release();
           const int nc = min(32, t.jv - c0);
           const int64_t row = t.jrow + c0;
-          const float sj = lane < nc && !empty ? gload(&a.j.s2[row + lane]) : 0.0f;
-          if (kGated) {
-            uint16_t* h = static_cast<uint16_t*>(a.out) + row * a.ni + n;
-            uint16_t* p = a.pre + row * (2 * static_cast<int64_t>(a.ni)) + n;
+          float y[32], z[32];
 #pragma unroll
-            for (int k = 0; k < 32; k++) {
-              const float s = __shfl_sync(0xFFFFFFFFu, sj, k);
-              const float gate = __uint_as_float(v[k]) * s * si, up = __uint_as_float(w[k]) * s * su;
-              if (k < nc && live) {
-                gstore(h, static_cast<uint16_t>(bf16x2_rn(silu(gate) * up, 0.0f)));
-                if (a.pre != nullptr) {
-                  const uint32_t b = bf16x2_rn(gate, up);
-                  gstore(p, static_cast<uint16_t>(b));
-                  gstore(p + a.ni, static_cast<uint16_t>(b >> 16));
-                }
-              }
-              h += a.ni;
-              p += 2 * static_cast<int64_t>(a.ni);
+          for (int k = 0; k < 32; k += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(sjw + k);
+            const float fk[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+              y[k + e] = __uint_as_float(v[k + e]) * fk[e] * si;
+              if (kGated) z[k + e] = __uint_as_float(w[k + e]) * fk[e] * su;
             }
+          }
+          if (empty) {
+#pragma unroll
+            for (int k = 0; k < 32; k++) y[k] = z[k] = 0.0f;
+          }
+          if (kGated) {
+            uint16_t* h = static_cast<uint16_t*>(a.out) + row * a.ni + t.i0 + 32 * q;
+            if (a.pre != nullptr) {
+              uint16_t* p = a.pre + row * (2 * static_cast<int64_t>(a.ni)) + t.i0 + 32 * q;
+              store_bf16(y, p, 2 * static_cast<int64_t>(a.ni), nc, t.iv - 32 * q, lane);
+              store_bf16(z, p + a.ni, 2 * static_cast<int64_t>(a.ni), nc, t.iv - 32 * q, lane);
+            }
+#pragma unroll
+            for (int k = 0; k < 32; k++) y[k] = silu(y[k]) * z[k];
+            store_bf16(y, h, a.ni, nc, t.iv - 32 * q, lane);
           } else {
-            float y[32];
-#pragma unroll
-            for (int k = 0; k < 32; k++) y[k] = __uint_as_float(v[k]) * __shfl_sync(0xFFFFFFFFu, sj, k) * si;
             if (kMode == kGemmAdapter) add_adapters(y, a, row, n, nc, lane, live);
-            float* f = static_cast<float*>(a.out) + row * a.ni + n;
-            uint16_t* h = static_cast<uint16_t*>(a.out) + row * a.ni + n;
+            if (a.out_f32) {
+              float* f = static_cast<float*>(a.out) + row * a.ni + n;
 #pragma unroll
-            for (int k = 0; k < 32; k++) {
-              if (k < nc && live) {
-                if (a.out_f32)
-                  gstore(f, y[k]);
-                else
-                  gstore(h, static_cast<uint16_t>(bf16x2_rn(y[k], 0.0f)));
+              for (int k = 0; k < 32; k++) {
+                if (k < nc && live) gstore(f, y[k]);
+                f += a.ni;
               }
-              f += a.ni;
-              h += a.ni;
+            } else {
+              store_bf16(y, static_cast<uint16_t*>(a.out) + row * a.ni + t.i0 + 32 * q, a.ni, nc, t.iv - 32 * q, lane);
             }
           }
         }
