@@ -35,10 +35,11 @@
 //   warp 0      data of each 256-element k block by TMA (128-byte swizzle) and
 //               tiled block scales by bulk copies
 //   warp 1      tensor memory, scale copies shared -> tensor memory, MMAs
-//   warps 2-5   what TMA cannot address: row-major block scales (4 bytes a row
-//               and k step into the 128x4 tiles the MMA wants) and, with
-//               kTma = false, the codes themselves (row strides that are not
-//               multiples of 16 bytes; wgrad's per-group strides)
+//   warps 2-5   what TMA cannot address: row-major block scales (16 bytes a row
+//               and k block, read one block ahead into registers and written
+//               as the 128x4 tiles the MMA wants) and, with kTma = false, the
+//               codes themselves (row strides that are not multiples of 16
+//               bytes; wgrad's per-group strides)
 //   warps 6-13  epilogue: two warps for each 32-lane quarter, alternate
 //               32-column chunks
 // Tensor memory holds two 256-column accumulators at columns 0 and 192 that
@@ -255,6 +256,29 @@ struct GemmWalk {
   }
 };
 
+// The k blocks of a CTA's tiles, one after the other.
+template <int kMode>
+struct GemmBlocks {
+  GemmWalk<kMode> walk;
+  GemmTile t;
+  int64_t ti;
+  int32_t kb, nkb;
+  bool more;
+  __device__ __forceinline__ GemmBlocks(const RoutingSmem& r, const GemmArgs& x) : walk(r, x), ti(blockIdx.x), kb(0) { tile(); }
+  __device__ __forceinline__ void tile() {
+    for (; (more = walk.seek(ti, t)); ti += gridDim.x) {
+      nkb = (t.kc + kGK - 1) / kGK;
+      if (nkb > 0) return;
+    }
+  }
+  __device__ __forceinline__ void next() {
+    if (++kb < nkb) return;
+    kb = 0;
+    ti += gridDim.x;
+    tile();
+  }
+};
+
 // ------------------------------------------------------------- loader roles
 
 // Row r of a k block's codes (kcopy: 16 or 8 bytes a copy) and its swizzled place.
@@ -275,40 +299,42 @@ __device__ __forceinline__ void load_codes(uint32_t dst, const uint8_t* data, in
   }
 }
 
-// Row-major block scales of `rows` rows and one k block (16 scales a row) into
-// 128x4 tiles: scale (r, 4 k + b) at tile k of the 128-row block, byte
-// (r % 32) * 16 + (r / 32) * 4 + b. Tile k of block q is tile q * 4 + k.
-__device__ __forceinline__ void load_scales(uint8_t* dst, const uint8_t* scale, int32_t cols, int rows, int32_t first,
-                                            int tid) {
-  for (int r = tid; r < rows; r += 128) {
-    uint8_t* d = dst + (r >> 7) * (4 * kGScaleTile) + (r & 31) * 16 + ((r & 127) >> 5) * 4;
-    const uint8_t* s = scale + static_cast<int64_t>(r) * cols + first;
-    if ((cols & 3) == 0) {
-      const uint32_t da = smem_addr(d);
+// The 16 block scales (one k block) of a row that has `left` scales from `src`
+// on, zeros behind its end. Wide loads where the rows' alignment allows: a
+// warp's 32 rows are 32 lines, and each load instruction pays for every line.
+__device__ __forceinline__ uint4 load_scale_row(const uint8_t* src, int32_t cols, int32_t left) {
+  if ((cols & 15) == 0) return gload(reinterpret_cast<const uint4*>(src));
+  uint32_t v[4];
+  if ((cols & 3) == 0) {
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
-        const bool in = first + 4 * k < cols;
-        cp_async<4>(da + k * kGScaleTile, in ? s + 4 * k : scale, in ? 4 : 0);
-      }
-    } else {
-      // rows start at any byte: the aligned words around the 16 bytes, shifted.
-      // A stacked matrix ends on a 16-byte boundary, so a word that holds a byte
-      // of it lies inside it.
-      const uint32_t sh = (reinterpret_cast<uintptr_t>(s) & 3) * 8;
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(s - (sh >> 3));
-      const int n = cols - first;  // bytes left in the row
-      uint32_t w[5];
+    for (int k = 0; k < 4; k++) v[k] = 4 * k < left ? gload(reinterpret_cast<const uint32_t*>(src) + k) : 0u;
+  } else {
+    // rows start at any byte: the aligned words around the 16 bytes, shifted. A
+    // stacked matrix ends on a 16-byte boundary, so a word that holds a byte of
+    // it lies inside it.
+    const uint32_t sh = (reinterpret_cast<uintptr_t>(src) & 3) * 8;
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(src - (sh >> 3));
+    uint32_t w[5];
 #pragma unroll
-      for (int k = 0; k < 5; k++) w[k] = 4 * k < n + static_cast<int>(sh >> 3) ? gload(p + k) : 0u;
+    for (int k = 0; k < 5; k++) w[k] = 4 * k < left + static_cast<int>(sh >> 3) ? gload(p + k) : 0u;
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
-        uint32_t v = __funnelshift_r(w[k], w[k + 1], sh);
-        const int left = n - 4 * k;
-        if (left < 4) v = left <= 0 ? 0u : v & (0xFFFFFFFFu >> (8 * (4 - left)));
-        *reinterpret_cast<uint32_t*>(d + k * kGScaleTile) = v;
-      }
+    for (int k = 0; k < 4; k++) {
+      v[k] = __funnelshift_r(w[k], w[k + 1], sh);
+      const int n = left - 4 * k;
+      if (n < 4) v[k] = n <= 0 ? 0u : v[k] & (0xFFFFFFFFu >> (8 * (4 - n)));
     }
   }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// Row r's 16 scales of a k block into 128x4 tiles: scale (r, 4 k + b) at tile k
+// of the 128-row block, byte (r % 32) * 16 + (r / 32) * 4 + b.
+__device__ __forceinline__ void store_scale_row(uint8_t* dst, int r, const uint4& v) {
+  uint8_t* d = dst + (r & 31) * 16 + (r >> 5) * 4;
+  *reinterpret_cast<uint32_t*>(d) = v.x;
+  *reinterpret_cast<uint32_t*>(d + kGScaleTile) = v.y;
+  *reinterpret_cast<uint32_t*>(d + 2 * kGScaleTile) = v.z;
+  *reinterpret_cast<uint32_t*>(d + 3 * kGScaleTile) = v.w;
 }
 
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
@@ -588,71 +614,103 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
       }
     } else if (warp >= kGLoadWarp && warp < kGEpiWarp && a.loaders) {
       const int tid = threadIdx.x - kGLoadWarp * 32;
-      GemmWalk<kMode> walk(sm.routing, a);
-      GemmTile t;
+      GemmBlocks<kMode> at(sm.routing, a);     // the block whose stage is filled
+      GemmBlocks<kMode> ahead(sm.routing, a);  // the block whose scales are read, one further
       uint32_t n = 0;
       bool ok = true;
+      // A thread's three rows of a stage's scales: row tid of each 128-row block
+      // (I, then two of J; gated: gate, up, J).
+      struct Rows {
+        uint4 v[3];
+      };
+      auto read = [&](GemmBlocks<kMode>& b, Rows& r) {
+        const GemmTile& t = b.t;
+        const int32_t cols = t.kc / 16, first = b.kb * 16, left = cols - first;
+        const uint8_t *is, *js;
+        if (kMode == kGemmWgrad) {
+          is = a.i.scale + t.goff * a.ni / 16 + static_cast<int64_t>(t.i0) * cols;
+          js = a.j.scale + t.goff * a.nj / 16 + static_cast<int64_t>(t.j0) * cols;
+        } else {
+          is = a.i.scale + t.irow * cols;
+          js = a.j.scale + t.jrow * cols;
+        }
+        is += static_cast<int64_t>(tid) * cols + first;
+        js += static_cast<int64_t>(tid) * cols + first;
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        constexpr int kJ = kGated ? 2 : 1;
+        r.v[0] = !a.i.tiled && tid < t.iv ? load_scale_row(is, cols, left) : zero;
+        if (kGated)
+          r.v[1] = !a.i.tiled && tid < t.iv ? load_scale_row(is + static_cast<int64_t>(a.ni) * cols, cols, left) : zero;
+        r.v[kJ] = !a.j.tiled && tid < t.jv ? load_scale_row(js, cols, left) : zero;
+        if (!kGated)
+          r.v[2] = !a.j.tiled && tid + 128 < t.jv ? load_scale_row(js + static_cast<int64_t>(128) * cols, cols, left) : zero;
+      };
       auto publish = [&](uint32_t k) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.full[k % kGStages]);
       };
-      for (int64_t ti = blockIdx.x; ok && walk.seek(ti, t); ti += gridDim.x) {
-        const int nkb = (t.kc + kGK - 1) / kGK;
-        const int64_t row_bytes = t.kc / 2;
-        const int32_t scols = t.kc / 16;
-        // base addresses of the tile's rows
-        const uint8_t *ic, *jc, *is, *js;
-        if (kMode == kGemmWgrad) {
-          ic = a.i.data + t.goff * a.ni / 2 + t.i0 * row_bytes;
-          jc = a.j.data + t.goff * a.nj / 2 + t.j0 * row_bytes;
-          is = a.i.scale + t.goff * a.ni / 16 + static_cast<int64_t>(t.i0) * scols;
-          js = a.j.scale + t.goff * a.nj / 16 + static_cast<int64_t>(t.j0) * scols;
-        } else {
-          ic = a.i.data + t.irow * row_bytes;
-          jc = a.j.data + t.jrow * row_bytes;
-          is = a.i.scale + t.irow * scols;
-          js = a.j.scale + t.jrow * scols;
+      Rows cur, nxt;
+      if (ahead.more) {
+        read(ahead, cur);
+        ahead.next();
+      }
+      for (; at.more; at.next(), n++) {
+        if (ahead.more) {
+          read(ahead, nxt);
+          ahead.next();
         }
-        for (int kb = 0; kb < nkb; kb++, n++) {
-          const int s = n % kGStages;
-          if (!mbar_wait(&sm.empty[s], ((n / kGStages) & 1) ^ 1)) {
-            ok = false;
-            break;
+        const int s = n % kGStages;
+        if (!mbar_wait(&sm.empty[s], ((n / kGStages) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        uint8_t* st = sm.stage[s];
+        if (!kTma) {
+          const GemmTile& t = at.t;
+          const int64_t row_bytes = t.kc / 2;
+          const uint8_t *ic, *jc;
+          if (kMode == kGemmWgrad) {
+            ic = a.i.data + t.goff * a.ni / 2 + t.i0 * row_bytes;
+            jc = a.j.data + t.goff * a.nj / 2 + t.j0 * row_bytes;
+          } else {
+            ic = a.i.data + t.irow * row_bytes;
+            jc = a.j.data + t.jrow * row_bytes;
           }
-          uint8_t* st = sm.stage[s];
-          if (!kTma) {
-            const uint32_t d = smem_addr(st);
-            const int cols = (t.jv + 15) & ~15;
-            if (row_bytes % 16 == 0) {
-              load_codes<16>(d, ic, row_bytes, kGI, t.iv, kb * 128, tid);
-              if (kGated) load_codes<16>(d + kGIBytes, ic + a.ni * row_bytes, row_bytes, kGI, t.iv, kb * 128, tid);
-              load_codes<16>(d + kIData, jc, row_bytes, cols, t.jv, kb * 128, tid);
-            } else {
-              load_codes<8>(d, ic, row_bytes, kGI, t.iv, kb * 128, tid);
-              if (kGated) load_codes<8>(d + kGIBytes, ic + a.ni * row_bytes, row_bytes, kGI, t.iv, kb * 128, tid);
-              load_codes<8>(d + kIData, jc, row_bytes, cols, t.jv, kb * 128, tid);
-            }
+          const uint32_t d = smem_addr(st);
+          const int cols = (t.jv + 15) & ~15, kbyte = at.kb * 128;
+          if (row_bytes % 16 == 0) {
+            load_codes<16>(d, ic, row_bytes, kGI, t.iv, kbyte, tid);
+            if (kGated) load_codes<16>(d + kGIBytes, ic + a.ni * row_bytes, row_bytes, kGI, t.iv, kbyte, tid);
+            load_codes<16>(d + kIData, jc, row_bytes, cols, t.jv, kbyte, tid);
+          } else {
+            load_codes<8>(d, ic, row_bytes, kGI, t.iv, kbyte, tid);
+            if (kGated) load_codes<8>(d + kGIBytes, ic + a.ni * row_bytes, row_bytes, kGI, t.iv, kbyte, tid);
+            load_codes<8>(d + kIData, jc, row_bytes, cols, t.jv, kbyte, tid);
           }
-          uint8_t* sf = st + kGDataBytes;
-          if (!a.i.tiled) {
-            load_scales(sf, is, scols, t.iv, kb * 16, tid);
-            if (kGated) load_scales(sf + 4 * kGScaleTile, is + static_cast<int64_t>(a.ni) * scols, scols, t.iv, kb * 16, tid);
-          }
-          if (!a.j.tiled) load_scales(sf + kISf, js, scols, t.jv, kb * 16, tid);
           cp_async_commit();
-          if (n >= kGLoadLag) {
-            cp_async_wait<kGLoadLag>();
-            publish(n - kGLoadLag);
-          }
+        }
+        uint8_t* sf = st + kGDataBytes;
+        if (!a.i.tiled) {
+          store_scale_row(sf, tid, cur.v[0]);
+          if (kGated) store_scale_row(sf + 4 * kGScaleTile, tid, cur.v[1]);
+        }
+        if (!a.j.tiled) {
+          store_scale_row(sf + kISf, tid, cur.v[kGated ? 2 : 1]);
+          if (!kGated && at.t.jv > 128) store_scale_row(sf + kISf + 4 * kGScaleTile, tid, cur.v[2]);
+        }
+        cur = nxt;
+        if (kTma) {
+          publish(n);
+        } else if (n >= kGLoadLag) {
+          cp_async_wait<kGLoadLag>();
+          publish(n - kGLoadLag);
         }
       }
       cp_async_wait<0>();
-      if (ok) {
+      if (!ok) sm.gave_up = 1;
+      else if (!kTma)
         for (uint32_t k = n > kGLoadLag ? n - kGLoadLag : 0; k < n; k++) publish(k);
-      } else {
-        sm.gave_up = 1;
-      }
     } else if (warp >= kGEpiWarp) {
       const int q = warp & 3;                       // accumulator lanes 32q .. 32q+31
       const int half = (warp - kGEpiWarp) >> 2;     // chunks of parity `half`
