@@ -30,11 +30,17 @@
 //
 // Work split. A persistent CTA per SM walks every gridDim-th tile (128 I rows
 // x `jt` J rows of one group, I tiles innermost so that concurrent CTAs share
-// the token tile and the group's weights in L2). Five roles, joined by
-// mbarriers:
+// the token tile and the group's weights in L2). Large problems run it on pairs
+// of CTAs (kPair): 256 I rows, 128 to a CTA, x up to 256 J rows of which each CTA
+// loads half, in one MMA over both SMs' tensor cores. What bounds a large product
+// is the 64 bytes a cycle at which an SM reads L2: a 256-element k block of
+// a 128 x 256 tile is 512 cycles of MMA and 54 KB (864 cycles) to one CTA, 38 KB
+// (608) to each of a pair. Five roles, joined by mbarriers:
 //   warp 0      data of each 256-element k block by TMA (128-byte swizzle) and
 //               tiled block scales by bulk copies
-//   warp 1      tensor memory, scale copies shared -> tensor memory, MMAs
+//   warp 1      tensor memory, scale copies shared -> tensor memory, MMAs (in
+//               a pair the first CTA's; the second's passes on that its stage
+//               has been filled)
 //   warps 2-5   what TMA cannot address: row-major block scales (16 bytes a row
 //               and k block, read one block ahead into registers and written
 //               as the 128x4 tiles the MMA wants) and, with kTma = false, the
@@ -66,21 +72,27 @@ constexpr int kGThreads = 448;       // 1 TMA + 1 MMA + 4 loader + 8 epilogue wa
 constexpr int kGLoadWarp = 2;
 constexpr int kGEpiWarp = 6;
 constexpr int kGEpiWarps = 8;
-constexpr int kGI = 128;             // I rows (accumulator lanes) of a tile
-constexpr int kGJ = 256;             // most J rows (accumulator columns) of a tile
+constexpr int kGI = 128;             // I rows (accumulator lanes) of a CTA's tile
 constexpr int kGK = 256;             // contraction elements of a stage: 128 bytes a row
-constexpr int kGStages = 4;
 constexpr int kGBigJ = 128;          // J rows of a TMA box ...
 constexpr int kGBoxJ = 32;           // ... and of one in a tile's rest
 constexpr int kGIBytes = kGI * 128;
-constexpr int kGJBytes = kGJ * 128;
 constexpr int kGScaleTile = 512;     // 128 rows x 4 scales
-constexpr int kGDataBytes = kGIBytes + kGJBytes;      // gated: two I tiles and half the J rows
-constexpr int kGSfBytes = 3 * 4 * kGScaleTile;        // I, and two blocks of 128 J rows, 4 k steps
-constexpr int kGStageBytes = kGDataBytes + kGSfBytes;
+constexpr int kGSfBytes = 3 * 4 * kGScaleTile;  // I and two blocks of 128 J rows (gated: gate, up, J), 4 k steps
 constexpr int kGAcc1 = 192;          // first column of the second accumulator
 constexpr int kGSfCol = 448;         // first scale column
 constexpr int kGLoadLag = 2;         // loader stages in flight before the oldest is published
+
+// A stage: I codes (gated: gate, then up), the CTA's J codes, scales.
+template <bool kGated>
+struct GemmStage {
+  static constexpr int kJRows = kGated ? 64 : 128;  // J rows a CTA holds; a pair's tile has twice as many
+  static constexpr int kIData = kGated ? 2 * kGIBytes : kGIBytes;
+  static constexpr int kData = kIData + kJRows * 128;
+  static constexpr int kISf = (kGated ? 2 : 1) * 4 * kGScaleTile;
+  static constexpr int kBytes = kData + kGSfBytes;
+  static constexpr int kStages = kGated ? 4 : 5;
+};
 
 struct GemmOperand {
   const uint8_t* data;
@@ -94,7 +106,8 @@ struct GemmArgs {
   int32_t ni;        // output columns: I rows of a group (gated: of each half)
   int32_t nj;        // wgrad: J rows of a group
   int32_t K;         // contraction (wgrad: the group's rows instead)
-  int32_t jt;        // J rows of a tile, a multiple of 16
+  int32_t jt;        // J rows of a tile: 32, 64, 128 or 256
+  int32_t jbulk;     // nonzero: J scales by bulk copies (tiled, and J tiles of whole 128-row blocks)
   int32_t loaders;   // nonzero: warps 2-5 take part
   int32_t producer;  // nonzero: warp 0 takes part
   int32_t out_f32;
@@ -108,21 +121,26 @@ struct GemmArgs {
   int32_t* status;         // or null
 };
 
+template <bool kGated>
 struct GemmSmem {
-  uint8_t stage[kGStages][kGStageBytes];
-  uint64_t full[kGStages];
-  uint64_t empty[kGStages];
+  using Stage = GemmStage<kGated>;
+  uint8_t stage[Stage::kStages][Stage::kBytes];
+  uint32_t turn[kGEpiWarps][16][32];     // an epilogue warp's chunk, row pairs x features
+  float sj[kGEpiWarps][32];              // the J factors of an epilogue warp's chunk
+  uint64_t full[Stage::kStages];
+  uint64_t peer_full[Stage::kStages];    // pair, first CTA: the second's stage is full
+  uint64_t empty[Stage::kStages];
   uint64_t acc_full;
-  uint64_t acc_free;
+  uint64_t acc_free;                     // pair: the first CTA's, for both epilogues
   uint64_t drain;
   uint32_t tmem;
   uint32_t gave_up;
   RoutingSmem routing;
-  alignas(16) float sj[kGEpiWarps][32];  // the J factors of each epilogue warp's chunk
 };
 
+template <bool kGated>
 constexpr size_t gemm_smem_bytes(int E) {
-  return ((sizeof(GemmSmem) + 15) & ~size_t{15}) + sizeof(int32_t) * (static_cast<size_t>(E) + 1);
+  return ((sizeof(GemmSmem<kGated>) + 15) & ~size_t{15}) + sizeof(int32_t) * (static_cast<size_t>(E) + 1);
 }
 
 // ------------------------------------------------------------------ tcgen05
@@ -139,19 +157,28 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
   return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (uint64_t{1} << 16) | (uint64_t{128 >> 4} << 32) |
          (uint64_t{1} << 46);
 }
-// Instruction descriptor of kind mxf4nvf4: E2M1 x E2M1, UE4M3 scales, M = 128,
-// N = n (a multiple of 16), both operands K-major.
+// Instruction descriptor of kind mxf4nvf4: E2M1 x E2M1, UE4M3 scales, M = 128
+// (256 in a pair), N = n (a multiple of 16), both operands K-major.
+template <bool kPair>
 __device__ __forceinline__ uint32_t mma_idesc(int n) {
-  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 27);
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((kPair ? 2u : 1u) << 27);
 }
 
+template <bool kPair>
 __device__ __forceinline__ void mma_nvf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                          uint32_t sfb, bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(static_cast<uint32_t>(accumulate))
-      : "memory");
+  if (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
 }
 // true in one lane of a converged warp
 __device__ __forceinline__ bool elect_one() {
@@ -159,12 +186,55 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
+// a 512-byte scale tile to four columns of every lane quarter (a pair: of both
+// CTAs, each from its own shared memory)
+template <bool kPair>
 __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  if (kPair)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
+// an arrival on `bar` (a pair: on both CTAs' one) once the MMAs issued so far are done
+template <bool kPair>
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-               : "memory");
+  if (kPair)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     smem_addr(bar)),
+                 "h"(static_cast<uint16_t>(3))
+                 : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot) {
+  if (kPair) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_dealloc(uint32_t tmem) {
+  if (kPair)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+// Arrival on the same barrier of the pair's first CTA. What it orders is not
+// this thread's own writes but the tensor core's and TMA's (already complete:
+// the thread has waited for them), so the default release is enough; one of
+// cluster scope flushes the thread's memory path and halved the product's rate.
+__device__ __forceinline__ void mbar_arrive_first(uint64_t* bar) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_addr(bar)));
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(at) : "memory");
+}
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -214,24 +284,28 @@ __device__ __forceinline__ void cp_async_wait() {
 
 struct GemmTile {
   int32_t kc;       // contraction length
-  int32_t i0, j0;   // first I and J row inside the group's matrices
-  int32_t iv, jv;   // I and J rows of the tile (iv <= 128, jv <= jt)
+  int32_t i0, j0;   // first I row of this CTA and first J row, inside the group's matrices
+  int32_t iv, jv;   // I rows of this CTA (0..128) and J rows of the tile (<= jt)
   int64_t irow;     // first I row: in the stacked matrix, or (wgrad) in the s2 vector
   int64_t jrow;     // first J row, likewise; also the output row
   int64_t goff;     // wgrad: the group's first routed row
 };
 
 // Forward-only walk: seek(t) for increasing t.
-template <int kMode>
+template <int kMode, bool kPair>
 struct GemmWalk {
   const RoutingSmem& rs;
   const GemmArgs& a;
+  static constexpr int kI = kPair ? 2 * kGI : kGI;  // I rows of a tile
   int32_t g = 0;
   int64_t before = 0;  // tiles of the groups before g
+  // tile indices: first() and then every step()-th; both CTAs of a pair take the same
+  __device__ __forceinline__ int64_t first() const { return kPair ? blockIdx.x >> 1 : blockIdx.x; }
+  __device__ __forceinline__ int64_t step() const { return kPair ? gridDim.x >> 1 : gridDim.x; }
   __device__ __forceinline__ GemmWalk(const RoutingSmem& r, const GemmArgs& x) : rs(r), a(x) {}
 
   __device__ __forceinline__ bool seek(int64_t t, GemmTile& tile) {
-    const int32_t it = (a.ni + kGI - 1) / kGI;
+    const int32_t it = (a.ni + kI - 1) / kI;
     int32_t m = 0;
     for (; g < rs.E; g++) {
       m = rs.off[g + 1] - rs.off[g];
@@ -244,9 +318,15 @@ struct GemmWalk {
     const int32_t jb = local / it, ib = local - jb * it;
     const int32_t jn = kMode == kGemmWgrad ? a.nj : m;
     tile.kc = kMode == kGemmWgrad ? m : a.K;
-    tile.i0 = ib * kGI;
-    tile.j0 = jb * a.jt;
+    tile.i0 = ib * kI;
     tile.iv = min(kGI, a.ni - tile.i0);
+    if (kPair && (blockIdx.x & 1)) {
+      // the second CTA's rows; with none left it works on the first's again and stores nothing
+      const int32_t left = a.ni - tile.i0 - kGI;
+      tile.iv = max(0, min(kGI, left));
+      if (left > 0) tile.i0 += kGI;
+    }
+    tile.j0 = jb * a.jt;
     tile.jv = min(a.jt, jn - tile.j0);
     tile.goff = rs.off[g];
     const int64_t in = kMode == kGemmGated ? int64_t{2} * a.ni : a.ni;
@@ -257,16 +337,16 @@ struct GemmWalk {
 };
 
 // The k blocks of a CTA's tiles, one after the other.
-template <int kMode>
+template <int kMode, bool kPair>
 struct GemmBlocks {
-  GemmWalk<kMode> walk;
+  GemmWalk<kMode, kPair> walk;
   GemmTile t;
   int64_t ti;
   int32_t kb, nkb;
   bool more;
-  __device__ __forceinline__ GemmBlocks(const RoutingSmem& r, const GemmArgs& x) : walk(r, x), ti(blockIdx.x), kb(0) { tile(); }
+  __device__ __forceinline__ GemmBlocks(const RoutingSmem& r, const GemmArgs& x) : walk(r, x), ti(walk.first()), kb(0) { tile(); }
   __device__ __forceinline__ void tile() {
-    for (; (more = walk.seek(ti, t)); ti += gridDim.x) {
+    for (; (more = walk.seek(ti, t)); ti += walk.step()) {
       nkb = (t.kc + kGK - 1) / kGK;
       if (nkb > 0) return;
     }
@@ -274,7 +354,7 @@ struct GemmBlocks {
   __device__ __forceinline__ void next() {
     if (++kb < nkb) return;
     kb = 0;
-    ti += gridDim.x;
+    ti += walk.step();
     tile();
   }
 };
@@ -327,6 +407,15 @@ __device__ __forceinline__ uint4 load_scale_row(const uint8_t* src, int32_t cols
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
+// The same of row r of a 128-row block of 128x4 tiles (`left` a multiple of 4).
+__device__ __forceinline__ uint4 load_tiled_row(const uint8_t* block, int r, int32_t left) {
+  const uint8_t* p = block + (r & 31) * 16 + (r >> 5) * 4;
+  uint32_t v[4];
+#pragma unroll
+  for (int k = 0; k < 4; k++) v[k] = 4 * k < left ? gload(reinterpret_cast<const uint32_t*>(p + k * kGScaleTile)) : 0u;
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
 // Row r's 16 scales of a k block into 128x4 tiles: scale (r, 4 k + b) at tile k
 // of the 128-row block, byte (r % 32) * 16 + (r / 32) * 4 + b.
 __device__ __forceinline__ void store_scale_row(uint8_t* dst, int r, const uint4& v) {
@@ -337,50 +426,50 @@ __device__ __forceinline__ void store_scale_row(uint8_t* dst, int r, const uint4
   *reinterpret_cast<uint32_t*>(d + 3 * kGScaleTile) = v.w;
 }
 
+__device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi2(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ uint64_t pair2(uint32_t lo, uint32_t hi) { return static_cast<uint64_t>(hi) << 32 | lo; }
+__device__ __forceinline__ uint32_t bf16_pair(uint64_t v) { return bf16x2_rn(lo2(v), hi2(v)); }
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
-// 32 rows x 32 features of a warp, lane = feature, y[k] = row k: rounded to bf16
-// and stored as 16 bytes (8 features) a lane. Three exchanges between lanes 1,
-// 2 and 4 apart turn columns into rows: after them, register block m of lane l
-// holds row 8 m + (l & 7), features (l & 24) .. + 7, so an instruction writes
-// 64 contiguous bytes of each of 8 rows. Stored one element a lane (2 bytes, 32
-// instructions and their predicates) a 128 x 256 tile took 15 k cycles.
-__device__ __forceinline__ void store_bf16(const float (&y)[32], uint16_t* out, int64_t pitch, int rows, int features,
-                                           int lane) {
-  uint32_t r[16];
-  const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
+// 32 rows x 32 features of a warp, lane = feature, y[i] = rows 2i and 2i + 1 as
+// bf16 pairs: turned in shared memory, stored as 16 bytes (8 features) a lane, so that
+// an instruction writes 64 contiguous bytes of each of 8 rows. Stored one
+// element a lane (2 bytes, 32 instructions and their predicates) a 128 x 256
+// tile took 15 k cycles, turned by lane exchanges 8 k.
+__device__ __forceinline__ void store_bf16(const uint32_t (&y)[16], uint32_t (&turn)[16][32], uint16_t* out,
+                                           int64_t pitch, int rows, int features, int lane) {
+  __syncwarp();  // the last chunk has been read
 #pragma unroll
-  for (int i = 0; i < 16; i++) {
-    const uint32_t p = bf16x2_rn(y[2 * i], y[2 * i + 1]);  // rows 2i (low), 2i + 1
-    const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, p, 1);
-    // even lanes: row 2i of (own, other); odd lanes: row 2i + 1 of (other, own)
-    r[i] = __byte_perm(p, o, b0 ? 0x3276 : 0x5410);
-  }
+  for (int i = 0; i < 16; i++) turn[i][lane] = y[i];
+  __syncwarp();
+  const int f = (lane & 3) * 8;
 #pragma unroll
-  for (int j = 0; j < 8; j++) {  // rows 4j + (lane & 3), four features
-    const uint32_t keep = b1 ? r[2 * j + 1] : r[2 * j], send = b1 ? r[2 * j] : r[2 * j + 1];
-    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, send, 2);
-    r[2 * j] = b1 ? got : keep;
-    r[2 * j + 1] = b1 ? keep : got;
-  }
-#pragma unroll
-  for (int m = 0; m < 4; m++) {  // rows 8m + (lane & 7), eight features
-    const uint32_t k0 = b2 ? r[4 * m + 2] : r[4 * m], k1 = b2 ? r[4 * m + 3] : r[4 * m + 1];
-    const uint32_t s0 = b2 ? r[4 * m] : r[4 * m + 2], s1 = b2 ? r[4 * m + 1] : r[4 * m + 3];
-    const uint32_t g0 = __shfl_xor_sync(0xFFFFFFFFu, s0, 4), g1 = __shfl_xor_sync(0xFFFFFFFFu, s1, 4);
-    const uint4 o = b2 ? make_uint4(g0, g1, k0, k1) : make_uint4(k0, k1, g0, g1);
-    const int row = 8 * m + (lane & 7);
-    if (row < rows && (lane & 24) < features)
-      gstore(reinterpret_cast<uint4*>(out + row * pitch + (lane & 24)), o);
+  for (int h = 0; h < 2; h++) {
+    const int i = 8 * h + (lane >> 2);
+    // odd row pairs read their second half first: two row pairs would share banks
+    const bool odd = i & 1;
+    const uint4 a = *reinterpret_cast<const uint4*>(&turn[i][f + (odd ? 4 : 0)]);
+    const uint4 b = *reinterpret_cast<const uint4*>(&turn[i][f + (odd ? 0 : 4)]);
+    const uint4 p = odd ? b : a, q = odd ? a : b;
+    const uint4 lo = make_uint4(__byte_perm(p.x, p.y, 0x5410), __byte_perm(p.z, p.w, 0x5410),
+                                __byte_perm(q.x, q.y, 0x5410), __byte_perm(q.z, q.w, 0x5410));
+    const uint4 hi = make_uint4(__byte_perm(p.x, p.y, 0x7632), __byte_perm(p.z, p.w, 0x7632),
+                                __byte_perm(q.x, q.y, 0x7632), __byte_perm(q.z, q.w, 0x7632));
+    if (f < features) {
+      uint16_t* o = out + 2 * i * pitch + f;
+      if (2 * i < rows) gstore(reinterpret_cast<uint4*>(o), lo);
+      if (2 * i + 1 < rows) gstore(reinterpret_cast<uint4*>(o + pitch), hi);
+    }
   }
 }
 
 // The adapters' share of a lane's 32 outputs (feature n of rows row .. row + nc - 1):
-// y[k] += sum_r u[row + k][r] b[id][n][r], in fp32, ranks in order in two
+// y[k] += sum_r u[row + k][r] b[id][n][r] (y2: pairs of rows), in fp32, ranks in order in two
 // interleaved sums (even and odd). Rows of one adapter, the rule in a prompt,
 // read the lane's row of B once; other rows read theirs eight ranks at a time,
 // several rows in flight.
-__device__ __forceinline__ void add_adapters(float (&y)[32], const GemmArgs& a, int64_t row, int64_t n, int nc, int lane,
+__device__ __forceinline__ void add_adapters(uint64_t (&y2)[16], const GemmArgs& a, int64_t row, int64_t n, int nc, int lane,
                                              bool live) {
   int32_t id = lane < nc ? gload(&a.ids[row + lane]) : -1;
   if (id < 0 || id >= a.adapters) id = -1;
@@ -393,7 +482,7 @@ __device__ __forceinline__ void add_adapters(float (&y)[32], const GemmArgs& a, 
   const int64_t pitch = static_cast<int64_t>(a.ni) * a.rank;
   uint64_t acc[32];
 #pragma unroll
-  for (int k = 0; k < 32; k++) acc[k] = pack2(y[k], 0.0f);
+  for (int k = 0; k < 32; k++) acc[k] = (k & 1 ? y2[k >> 1] >> 32 : y2[k >> 1] & 0xFFFFFFFFu);
   auto dot8 = [&](uint64_t& c, const uint4& w, const float* up) {
     const float4 u0 = gload(reinterpret_cast<const float4*>(up)), u1 = gload(reinterpret_cast<const float4*>(up) + 1);
     c = fma2x(pack2(u0.x, u0.y), unpack2(w.x), c);
@@ -424,8 +513,7 @@ __device__ __forceinline__ void add_adapters(float (&y)[32], const GemmArgs& a, 
     }
   }
 #pragma unroll
-  for (int k = 0; k < 32; k++)
-    y[k] = __uint_as_float(static_cast<uint32_t>(acc[k])) + __uint_as_float(static_cast<uint32_t>(acc[k] >> 32));
+  for (int k = 0; k < 16; k++) y2[k] = pack2(lo2(acc[2 * k]) + hi2(acc[2 * k]), lo2(acc[2 * k + 1]) + hi2(acc[2 * k + 1]));
 }
 
 // One stage's scale copies and MMAs, by one thread. All descriptors are one
@@ -433,89 +521,89 @@ __device__ __forceinline__ void add_adapters(float (&y)[32], const GemmArgs& a, 
 // instruction costs about 70 cycles of issue for each copy or MMA, more than the
 // 128 cycles an N = 256 MMA runs (measured: 12 copies and 4 MMAs 1070 cycles
 // a stage so, 513 as here, which is the MMAs alone).
-template <bool kGated, bool kFull>
+template <bool kGated, bool kPair, bool kFull>
 __device__ __forceinline__ void issue_stage(uint32_t st, uint32_t tmem, uint32_t acc, uint32_t idesc, int ksteps,
                                             bool two, bool first) {
-  constexpr int kIData = kGated ? 2 * kGIBytes : kGIBytes;
-  constexpr int kISf = (kGated ? 2 : 1) * 4 * kGScaleTile;
+  using Stage = GemmStage<kGated>;
   constexpr int kTileUnits = kGScaleTile >> 4;
   constexpr int kJCols = kGated ? 4 : 8;
-  const uint64_t di = mma_desc(st), dj = mma_desc(st + kIData);
-  const uint64_t si = scale_desc(st + kGDataBytes), sj = scale_desc(st + kGDataBytes + kISf);
+  const uint64_t di = mma_desc(st), dj = mma_desc(st + Stage::kIData);
+  const uint64_t si = scale_desc(st + Stage::kData), sj = scale_desc(st + Stage::kData + Stage::kISf);
   const uint32_t ti = tmem + kGSfCol, tj = ti + (kGated ? 32 : 16);
 #pragma unroll
   for (int k = 0; k < 4; k++)
     if (kFull || k < ksteps) {
-      tmem_copy_scales(ti + 4 * k, si + kTileUnits * k);
-      if (kGated) tmem_copy_scales(ti + 16 + 4 * k, si + kTileUnits * (4 + k));
-      tmem_copy_scales(tj + kJCols * k, sj + kTileUnits * k);
+      tmem_copy_scales<kPair>(ti + 4 * k, si + kTileUnits * k);
+      if (kGated) tmem_copy_scales<kPair>(ti + 16 + 4 * k, si + kTileUnits * (4 + k));
+      tmem_copy_scales<kPair>(tj + kJCols * k, sj + kTileUnits * k);
     }
   if (!kGated && two) {
 #pragma unroll
     for (int k = 0; k < 4; k++)
-      if (kFull || k < ksteps) tmem_copy_scales(tj + 8 * k + 4, sj + kTileUnits * (4 + k));
+      if (kFull || k < ksteps) tmem_copy_scales<kPair>(tj + 8 * k + 4, sj + kTileUnits * (4 + k));
   }
 #pragma unroll
   for (int k = 0; k < 4; k++)
     if (kFull || k < ksteps) {
-      mma_nvf4(acc, di + 2 * k, dj + 2 * k, idesc, ti + 4 * k, tj + kJCols * k, !first || k > 0);
+      mma_nvf4<kPair>(acc, di + 2 * k, dj + 2 * k, idesc, ti + 4 * k, tj + kJCols * k, !first || k > 0);
       if (kGated)
-        mma_nvf4(acc + 128, di + (kGIBytes >> 4) + 2 * k, dj + 2 * k, idesc, ti + 16 + 4 * k, tj + kJCols * k,
-                 !first || k > 0);
+        mma_nvf4<kPair>(acc + 128, di + (kGIBytes >> 4) + 2 * k, dj + 2 * k, idesc, ti + 16 + 4 * k, tj + kJCols * k,
+                        !first || k > 0);
     }
 }
 
 // ------------------------------------------------------------------ kernel
 
-template <class Routing, int kMode, bool kTma>
+template <class Routing, int kMode, bool kTma, bool kPair>
 __global__ void __launch_bounds__(kGThreads, 1)
 group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant__ CUtensorMap imap,
                   const __grid_constant__ CUtensorMap jmap, const __grid_constant__ CUtensorMap jmap_small,
                   const __grid_constant__ GemmArgs a) {
   constexpr bool kGated = kMode == kGemmGated;
+  using Stage = GemmStage<kGated>;
+  using Walk = GemmWalk<kMode, kPair>;
+  constexpr int kStages = Stage::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  GemmSmem& sm = *reinterpret_cast<GemmSmem*>(base);
-  int32_t* off = reinterpret_cast<int32_t*>(base + ((sizeof(GemmSmem) + 15) & ~size_t{15}));
+  GemmSmem<kGated>& sm = *reinterpret_cast<GemmSmem<kGated>*>(base);
+  int32_t* off = reinterpret_cast<int32_t*>(base + ((sizeof(GemmSmem<kGated>) + 15) & ~size_t{15}));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = kPair ? static_cast<int>(blockIdx.x & 1) : 0;  // in the pair
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kGStages; s++) {
+    for (int s = 0; s < kStages; s++) {
       mbar_init(&sm.full[s], (a.producer ? 1 : 0) + (a.loaders ? 4 : 0));
+      mbar_init(&sm.peer_full[s], 1);
       mbar_init(&sm.empty[s], 1);
     }
     mbar_init(&sm.acc_full, 1);
-    mbar_init(&sm.acc_free, kGEpiWarps);
+    mbar_init(&sm.acc_free, kGEpiWarps * (kPair ? 2 : 1));
     mbar_init(&sm.drain, 1);
     sm.gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sm.tmem))
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tmem_alloc<kPair>(&sm.tmem);
     tc_fence_before();
   }
   routing.load(sm.routing, off);  // ends with a __syncthreads
+  if (kPair) pair_sync();         // the other CTA's barriers are initialised, its tensor memory allocated
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sm.tmem);
 
-  // stage layout: I codes (gated: gate then up), J codes, I scales (likewise), J scales
-  constexpr int kIData = kGated ? 2 * kGIBytes : kGIBytes;
-  constexpr int kISf = (kGated ? 2 : 1) * 4 * kGScaleTile;
-
   if (sm.routing.ok) {
     if (warp == 0 && a.producer) {
-      GemmWalk<kMode> walk(sm.routing, a);
+      Walk walk(sm.routing, a);
       GemmTile t;
       const bool elected = elect_one();
       uint32_t n = 0;
       bool ok = true;
       const uint64_t pol = policy_evict_normal();
-      for (int64_t ti = blockIdx.x; ok && walk.seek(ti, t); ti += gridDim.x) {
+      for (int64_t ti = walk.first(); ok && walk.seek(ti, t); ti += walk.step()) {
         const int nkb = (t.kc + kGK - 1) / kGK;
-        // J rows: boxes of 128, the rest in boxes of 32
-        const int big = t.jv / kGBigJ, small = (t.jv - big * kGBigJ + kGBoxJ - 1) / kGBoxJ;
+        // this CTA's J rows: boxes of 128, the rest in boxes of 32
+        const int jrows = kPair ? ((t.jv + 31) & ~31) / 2 : t.jv;
+        const int big = jrows / kGBigJ, small = (jrows - big * kGBigJ + kGBoxJ - 1) / kGBoxJ;
         const int jblocks = (t.jv + 127) / 128;
         const int64_t kt = t.kc / 64;
         // tiled scales: tile (row block, k step) at (block * kc/64 + step) * 512
@@ -523,14 +611,14 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
                                                              : t.irow / 128 * kt * kGScaleTile);
         const uint8_t* js = a.j.scale + (kMode == kGemmWgrad ? t.goff * a.nj / 16 + t.j0 / 128 * kt * kGScaleTile
                                                              : t.jrow / 128 * kt * kGScaleTile);
-        const int iy = static_cast<int>(t.irow), jy = static_cast<int>(t.jrow);
+        const int iy = static_cast<int>(t.irow), jy = static_cast<int>(t.jrow) + rank * jrows;
         uint32_t data_bytes = 0, tiles = 0;
         if (kTma) data_bytes = (kGated ? 2 : 1) * kGIBytes + (big * kGBigJ + small * kGBoxJ) * 128;
         if (a.i.tiled) tiles += kGated ? 2 : 1;
-        if (a.j.tiled) tiles += jblocks;
+        if (a.jbulk) tiles += jblocks;
         for (int kb = 0; kb < nkb; kb++, n++) {
-          const int s = n % kGStages;
-          if (!mbar_wait(&sm.empty[s], ((n / kGStages) & 1) ^ 1)) {
+          const int s = n % kStages;
+          if (!mbar_wait(&sm.empty[s], ((n / kStages) & 1) ^ 1)) {
             ok = false;
             break;
           }
@@ -543,37 +631,50 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
               tma_load_2d(st, &imap, kb * 128, iy, bar, pol);
               if (kGated) tma_load_2d(st + kGIBytes, &imap, kb * 128, iy + a.ni, bar, pol);
               for (int b = 0; b < big; b++)
-                tma_load_2d(st + kIData + b * kGBigJ * 128, &jmap, kb * 128, jy + b * kGBigJ, bar, pol);
+                tma_load_2d(st + Stage::kIData + b * kGBigJ * 128, &jmap, kb * 128, jy + b * kGBigJ, bar, pol);
               for (int b = 0; b < small; b++)
-                tma_load_2d(st + kIData + (big * kGBigJ + b * kGBoxJ) * 128, &jmap_small, kb * 128,
+                tma_load_2d(st + Stage::kIData + (big * kGBigJ + b * kGBoxJ) * 128, &jmap_small, kb * 128,
                             jy + big * kGBigJ + b * kGBoxJ, bar, pol);
             }
-            uint8_t* sf = st + kGDataBytes;
+            uint8_t* sf = st + Stage::kData;
             const int32_t so = kb * 4 * kGScaleTile;
             if (a.i.tiled) {
               bulk_load(sf, is + so, sf_bytes, bar);
               if (kGated) bulk_load(sf + 4 * kGScaleTile, is + a.ni / 128 * kt * kGScaleTile + so, sf_bytes, bar);
             }
-            if (a.j.tiled)
+            if (a.jbulk)
               for (int b = 0; b < jblocks; b++)
-                bulk_load(sf + kISf + b * 4 * kGScaleTile, js + b * kt * kGScaleTile + so, sf_bytes, bar);
+                bulk_load(sf + Stage::kISf + b * 4 * kGScaleTile, js + b * kt * kGScaleTile + so, sf_bytes, bar);
           }
           __syncwarp();
         }
       }
       if (!ok) {
         sm.gave_up = 1;
-        for (uint32_t k = n > kGStages ? n - kGStages : 0; k < n; k++)
-          mbar_wait(&sm.full[k % kGStages], (k / kGStages) & 1);
+        for (uint32_t k = n > kStages ? n - kStages : 0; k < n; k++)
+          mbar_wait(&sm.full[k % kStages], (k / kStages) & 1);
+      }
+    } else if (warp == 1 && rank == 1) {
+      // second CTA of a pair: tells the first that a stage is full
+      GemmBlocks<kMode, kPair> at(sm.routing, a);
+      const bool elected = elect_one();
+      for (uint32_t n = 0; at.more; at.next(), n++) {
+        const int s = n % kStages;
+        if (!mbar_wait(&sm.full[s], (n / kStages) & 1)) {
+          sm.gave_up = 1;
+          break;
+        }
+        if (elected) mbar_arrive_first(&sm.peer_full[s]);
+        __syncwarp();
       }
     } else if (warp == 1) {
-      GemmWalk<kMode> walk(sm.routing, a);
+      Walk walk(sm.routing, a);
       GemmTile t;
       const bool elected = elect_one();
       uint32_t n = 0, tiles = 0;
       bool ok = true;
       const uint32_t stages = smem_addr(sm.stage[0]);
-      for (int64_t ti = blockIdx.x; ok && walk.seek(ti, t); ti += gridDim.x) {
+      for (int64_t ti = walk.first(); ok && walk.seek(ti, t); ti += walk.step()) {
         const int nkb = (t.kc + kGK - 1) / kGK;
         if (nkb == 0) continue;
         if (tiles > 0 && !mbar_wait(&sm.acc_free, (tiles - 1) & 1)) {
@@ -582,40 +683,41 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
         }
         tc_fence_after();
         const uint32_t acc = tmem + ((tiles & 1) ? kGAcc1 : 0);
-        const int cols = (t.jv + 15) & ~15;
-        const uint32_t idesc = mma_idesc(cols);
+        const int cols = kPair ? (t.jv + 31) & ~31 : (t.jv + 15) & ~15;
+        const uint32_t idesc = mma_idesc<kPair>(cols);
         for (int kb = 0; kb < nkb; kb++, n++) {
-          const int s = n % kGStages;
-          if (!mbar_wait(&sm.full[s], (n / kGStages) & 1)) {
+          const int s = n % kStages;
+          if (!mbar_wait(&sm.full[s], (n / kStages) & 1) ||
+              (kPair && !mbar_wait(&sm.peer_full[s], (n / kStages) & 1))) {
             ok = false;
             break;
           }
           tc_fence_after();
           const int ksteps = min(4, (t.kc - kb * kGK + 63) / 64);
           if (elected) {
-            const uint32_t st = stages + s * kGStageBytes;
+            const uint32_t st = stages + s * Stage::kBytes;
             if (ksteps == 4)
-              issue_stage<kGated, true>(st, tmem, acc, idesc, 4, cols > 128, kb == 0);
+              issue_stage<kGated, kPair, true>(st, tmem, acc, idesc, 4, cols > 128, kb == 0);
             else
-              issue_stage<kGated, false>(st, tmem, acc, idesc, ksteps, cols > 128, kb == 0);
-            mma_commit(&sm.empty[s]);
+              issue_stage<kGated, kPair, false>(st, tmem, acc, idesc, ksteps, cols > 128, kb == 0);
+            mma_commit<kPair>(&sm.empty[s]);
           }
           __syncwarp();
         }
-        if (ok && elected) mma_commit(&sm.acc_full);
+        if (ok && elected) mma_commit<kPair>(&sm.acc_full);
         __syncwarp();
         tiles++;
       }
       if (!ok) {
         sm.gave_up = 1;
-        if (elected) mma_commit(&sm.drain);
+        if (elected) mma_commit<kPair>(&sm.drain);
         __syncwarp();
         mbar_wait(&sm.drain, 0);
       }
     } else if (warp >= kGLoadWarp && warp < kGEpiWarp && a.loaders) {
       const int tid = threadIdx.x - kGLoadWarp * 32;
-      GemmBlocks<kMode> at(sm.routing, a);     // the block whose stage is filled
-      GemmBlocks<kMode> ahead(sm.routing, a);  // the block whose scales are read, one further
+      GemmBlocks<kMode, kPair> at(sm.routing, a);     // the block whose stage is filled
+      GemmBlocks<kMode, kPair> ahead(sm.routing, a);  // the block whose scales are read, one further
       uint32_t n = 0;
       bool ok = true;
       // A thread's three rows of a stage's scales: row tid of each 128-row block
@@ -623,7 +725,7 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
       struct Rows {
         uint4 v[3];
       };
-      auto read = [&](GemmBlocks<kMode>& b, Rows& r) {
+      auto read = [&](GemmBlocks<kMode, kPair>& b, Rows& r) {
         const GemmTile& t = b.t;
         const int32_t cols = t.kc / 16, first = b.kb * 16, left = cols - first;
         const uint8_t *is, *js;
@@ -641,14 +743,24 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
         r.v[0] = !a.i.tiled && tid < t.iv ? load_scale_row(is, cols, left) : zero;
         if (kGated)
           r.v[1] = !a.i.tiled && tid < t.iv ? load_scale_row(is + static_cast<int64_t>(a.ni) * cols, cols, left) : zero;
-        r.v[kJ] = !a.j.tiled && tid < t.jv ? load_scale_row(js, cols, left) : zero;
-        if (!kGated)
-          r.v[2] = !a.j.tiled && tid + 128 < t.jv ? load_scale_row(js + static_cast<int64_t>(128) * cols, cols, left) : zero;
+        if (a.j.tiled) {
+          // a J tile inside a 128-row block (jt < 128): its rows out of the block's
+          // tiles. The scales in tensor memory cannot start at a later column.
+          if (!a.jbulk) {
+            const int64_t kt = t.kc / 64;
+            const uint8_t* tb = a.j.scale + (kMode == kGemmWgrad ? t.goff * a.nj / 16 + t.j0 / 128 * kt * kGScaleTile
+                                                                 : t.jrow / 128 * kt * kGScaleTile);
+            r.v[kJ] = tid < t.jv ? load_tiled_row(tb + b.kb * 4 * kGScaleTile, (t.j0 & 127) + tid, left) : zero;
+          }
+        } else {
+          r.v[kJ] = tid < t.jv ? load_scale_row(js, cols, left) : zero;
+          if (!kGated) r.v[2] = tid + 128 < t.jv ? load_scale_row(js + static_cast<int64_t>(128) * cols, cols, left) : zero;
+        }
       };
       auto publish = [&](uint32_t k) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.full[k % kGStages]);
+        if (lane == 0) mbar_arrive(&sm.full[k % kStages]);
       };
       Rows cur, nxt;
       if (ahead.more) {
@@ -660,8 +772,8 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
           read(ahead, nxt);
           ahead.next();
         }
-        const int s = n % kGStages;
-        if (!mbar_wait(&sm.empty[s], ((n / kGStages) & 1) ^ 1)) {
+        const int s = n % kStages;
+        if (!mbar_wait(&sm.empty[s], ((n / kStages) & 1) ^ 1)) {
           ok = false;
           break;
         }
@@ -678,26 +790,29 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
             jc = a.j.data + t.jrow * row_bytes;
           }
           const uint32_t d = smem_addr(st);
-          const int cols = (t.jv + 15) & ~15, kbyte = at.kb * 128;
+          // this CTA's J rows
+          const int cols = kPair ? ((t.jv + 31) & ~31) / 2 : (t.jv + 15) & ~15, kbyte = at.kb * 128;
+          const int jv = max(0, min(cols, t.jv - rank * cols));
+          jc += rank * cols * row_bytes;
           if (row_bytes % 16 == 0) {
             load_codes<16>(d, ic, row_bytes, kGI, t.iv, kbyte, tid);
             if (kGated) load_codes<16>(d + kGIBytes, ic + a.ni * row_bytes, row_bytes, kGI, t.iv, kbyte, tid);
-            load_codes<16>(d + kIData, jc, row_bytes, cols, t.jv, kbyte, tid);
+            load_codes<16>(d + Stage::kIData, jc, row_bytes, cols, jv, kbyte, tid);
           } else {
             load_codes<8>(d, ic, row_bytes, kGI, t.iv, kbyte, tid);
             if (kGated) load_codes<8>(d + kGIBytes, ic + a.ni * row_bytes, row_bytes, kGI, t.iv, kbyte, tid);
-            load_codes<8>(d + kIData, jc, row_bytes, cols, t.jv, kbyte, tid);
+            load_codes<8>(d + Stage::kIData, jc, row_bytes, cols, jv, kbyte, tid);
           }
           cp_async_commit();
         }
-        uint8_t* sf = st + kGDataBytes;
+        uint8_t* sf = st + Stage::kData;
         if (!a.i.tiled) {
           store_scale_row(sf, tid, cur.v[0]);
           if (kGated) store_scale_row(sf + 4 * kGScaleTile, tid, cur.v[1]);
         }
-        if (!a.j.tiled) {
-          store_scale_row(sf + kISf, tid, cur.v[kGated ? 2 : 1]);
-          if (!kGated && at.t.jv > 128) store_scale_row(sf + kISf + 4 * kGScaleTile, tid, cur.v[2]);
+        if (!a.jbulk) {
+          store_scale_row(sf + Stage::kISf, tid, cur.v[kGated ? 2 : 1]);
+          if (!kGated && at.t.jv > 128) store_scale_row(sf + Stage::kISf + 4 * kGScaleTile, tid, cur.v[2]);
         }
         cur = nxt;
         if (kTma) {
@@ -714,31 +829,49 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
     } else if (warp >= kGEpiWarp) {
       const int q = warp & 3;                       // accumulator lanes 32q .. 32q+31
       const int half = (warp - kGEpiWarp) >> 2;     // chunks of parity `half`
-      GemmWalk<kMode> walk(sm.routing, a);
-      GemmTile t;
-      uint32_t tiles = 0;
-      for (int64_t ti = blockIdx.x; walk.seek(ti, t); ti += gridDim.x) {
-        const bool empty = t.kc == 0;
-        const int il = 32 * q + lane;
-        const int64_t n = t.i0 + il;
-        const bool live = il < t.iv;
-        float si = 0.0f, su = 0.0f;
-        if (live && !empty) {
-          si = gload(&a.i.s2[t.irow + il]);
-          if (kGated) su = gload(&a.i.s2[t.irow + a.ni + il]);
+      const int il = 32 * q + lane;
+      // chunks of 32 columns; the first one a warp takes holds its part of
+      // the columns both accumulators share (set 0: the last two, set 1: the
+      // first two; gated: of the up or the gate half)
+      constexpr int kChunks = kGated ? 4 : 8, kMine = kChunks / 2;
+      auto chunk = [&](int set, int ci) { return (set == 0 ? (ci == 0 ? kChunks - 2 : 2 * (ci - 1)) : 2 * ci) + half; };
+      // a tile's factors, read before the tile before it is finished
+      struct Factors {
+        float i, up;
+        float j[kMine];
+      };
+      auto read = [&](const GemmTile& t, int set, Factors& f) {
+        f.i = f.up = 0.0f;
+        if (il < t.iv) {
+          f.i = gload(&a.i.s2[t.irow + il]);
+          if (kGated) f.up = gload(&a.i.s2[t.irow + a.ni + il]);
         }
-        const int set = tiles & 1;
-        // chunks of 32 columns; the first one a warp takes holds its part of
-        // the columns both accumulators share (set 0: the last two, set 1: the
-        // first two; gated: of the up or the gate half)
-        constexpr int kChunks = kGated ? 4 : 8;
-        auto chunk = [&](int ci) { return (set == 0 ? (ci == 0 ? kChunks - 2 : 2 * (ci - 1)) : 2 * ci) + half; };
-        float sj[kChunks / 2];
 #pragma unroll
-        for (int ci = 0; ci < kChunks / 2; ci++) {
-          const int c = chunk(ci) * 32 + lane;
-          sj[ci] = c < t.jv && !empty ? gload(&a.j.s2[t.jrow + c]) : 0.0f;
+        for (int ci = 0; ci < kMine; ci++) {
+          const int c = chunk(set, ci) * 32 + lane;
+          f.j[ci] = c < t.jv ? gload(&a.j.s2[t.jrow + c]) : 0.0f;
         }
+      };
+      Walk walk(sm.routing, a);
+      GemmTile t, t1;
+      Factors f{}, f1{};
+      uint32_t tiles = 0;
+      int64_t ti = walk.first();
+      bool more = walk.seek(ti, t1);
+      if (more && t1.kc > 0) read(t1, 0, f1);
+      float* sjw = sm.sj[warp - kGEpiWarp];
+      uint32_t(&turn)[16][32] = sm.turn[warp - kGEpiWarp];
+      while (more) {
+        t = t1;
+        f = f1;
+        const bool empty = t.kc == 0;
+        ti += walk.step();
+        more = walk.seek(ti, t1);
+        f1 = Factors{};
+        if (more && t1.kc > 0) read(t1, (tiles + (empty ? 0 : 1)) & 1, f1);
+        const bool live = il < t.iv;
+        const int64_t n = t.i0 + il;
+        const int set = tiles & 1;
         if (!empty) {
           if (!mbar_wait(&sm.acc_full, tiles & 1)) {
             if (lane == 0) sm.gave_up = 1;
@@ -748,19 +881,24 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
         }
         if (kMode == kGemmAdapter) grid_dependency_wait();  // u comes from the kernel before this one
         const uint32_t acc = tmem + (set ? kGAcc1 : 0) + (static_cast<uint32_t>(32 * q) << 16);
-        float* sjw = sm.sj[warp - kGEpiWarp];
+        const uint64_t si2 = pack2(f.i, f.i), su2 = pack2(f.up, f.up);
         bool freed = empty;
         auto release = [&] {
           if (!freed) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.acc_free);
+            if (lane == 0) {
+              if (kPair)
+                mbar_arrive_first(&sm.acc_free);
+              else
+                mbar_arrive(&sm.acc_free);
+            }
             freed = true;
           }
         };
 #pragma unroll 1
-        for (int ci = 0; ci < kChunks / 2; ci++) {
-          const int c0 = chunk(ci) * 32;
+        for (int ci = 0; ci < kMine; ci++) {
+          const int c0 = chunk(set, ci) * 32;
           if (c0 >= t.jv) {
             if (ci == 0) release();
             continue;
@@ -772,51 +910,62 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
           } else {
             tmem_load32(acc + c0, v);
             if (kGated) tmem_load32(acc + 128 + c0, w);
-            __syncwarp();  // the previous chunk's factors have been read
-            sjw[lane] = ci == 0 ? sj[0] : ci == 1 ? sj[1] : ci == 2 ? sj[kChunks / 2 > 2 ? 2 : 0] : sj[kChunks / 2 - 1];
-            __syncwarp();
+          }
+          float fj = f.j[0];
+#pragma unroll
+          for (int k = 1; k < kMine; k++)
+            if (ci == k) fj = f.j[k];
+          __syncwarp();  // the previous chunk's factors have been read
+          sjw[lane] = empty ? 0.0f : fj;
+          __syncwarp();
+          if (!empty) {
             tmem_load_wait(v);
             if (kGated) tmem_load_wait(w);
           }
           if (ci == 0) release();
           const int nc = min(32, t.jv - c0);
           const int64_t row = t.jrow + c0;
-          float y[32], z[32];
+          uint64_t y[16], z[16];  // rows 2k and 2k + 1
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(sjw + k);
-            const float fk[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-              y[k + e] = __uint_as_float(v[k + e]) * fk[e] * si;
-              if (kGated) z[k + e] = __uint_as_float(w[k + e]) * fk[e] * su;
+          for (int k = 0; k < 16; k += 2) {
+            const float4 s = *reinterpret_cast<const float4*>(sjw + 2 * k);
+            const uint64_t s0 = pack2(s.x, s.y), s1 = pack2(s.z, s.w);
+            y[k] = mul2x(mul2x(pair2(v[2 * k], v[2 * k + 1]), s0), si2);
+            y[k + 1] = mul2x(mul2x(pair2(v[2 * k + 2], v[2 * k + 3]), s1), si2);
+            if (kGated) {
+              z[k] = mul2x(mul2x(pair2(w[2 * k], w[2 * k + 1]), s0), su2);
+              z[k + 1] = mul2x(mul2x(pair2(w[2 * k + 2], w[2 * k + 3]), s1), su2);
             }
           }
-          if (empty) {
-#pragma unroll
-            for (int k = 0; k < 32; k++) y[k] = z[k] = 0.0f;
-          }
+          const int features = t.iv - 32 * q;
+          uint32_t b[16];
           if (kGated) {
-            uint16_t* h = static_cast<uint16_t*>(a.out) + row * a.ni + t.i0 + 32 * q;
             if (a.pre != nullptr) {
-              uint16_t* p = a.pre + row * (2 * static_cast<int64_t>(a.ni)) + t.i0 + 32 * q;
-              store_bf16(y, p, 2 * static_cast<int64_t>(a.ni), nc, t.iv - 32 * q, lane);
-              store_bf16(z, p + a.ni, 2 * static_cast<int64_t>(a.ni), nc, t.iv - 32 * q, lane);
+              const int64_t pitch = 2 * static_cast<int64_t>(a.ni);
+              uint16_t* p = a.pre + row * pitch + t.i0 + 32 * q;
+#pragma unroll
+              for (int k = 0; k < 16; k++) b[k] = bf16_pair(y[k]);
+              store_bf16(b, turn, p, pitch, nc, features, lane);
+#pragma unroll
+              for (int k = 0; k < 16; k++) b[k] = bf16_pair(z[k]);
+              store_bf16(b, turn, p + a.ni, pitch, nc, features, lane);
             }
 #pragma unroll
-            for (int k = 0; k < 32; k++) y[k] = silu(y[k]) * z[k];
-            store_bf16(y, h, a.ni, nc, t.iv - 32 * q, lane);
+            for (int k = 0; k < 16; k++) b[k] = bf16x2_rn(silu(lo2(y[k])) * lo2(z[k]), silu(hi2(y[k])) * hi2(z[k]));
+            store_bf16(b, turn, static_cast<uint16_t*>(a.out) + row * a.ni + t.i0 + 32 * q, a.ni, nc, features, lane);
           } else {
             if (kMode == kGemmAdapter) add_adapters(y, a, row, n, nc, lane, live);
             if (a.out_f32) {
-              float* f = static_cast<float*>(a.out) + row * a.ni + n;
+              float* o = static_cast<float*>(a.out) + row * a.ni + n;
 #pragma unroll
               for (int k = 0; k < 32; k++) {
-                if (k < nc && live) gstore(f, y[k]);
-                f += a.ni;
+                if (k < nc && live) gstore(o, k & 1 ? hi2(y[k >> 1]) : lo2(y[k >> 1]));
+                o += a.ni;
               }
             } else {
-              store_bf16(y, static_cast<uint16_t*>(a.out) + row * a.ni + t.i0 + 32 * q, a.ni, nc, t.iv - 32 * q, lane);
+#pragma unroll
+              for (int k = 0; k < 16; k++) b[k] = bf16_pair(y[k]);
+              store_bf16(b, turn, static_cast<uint16_t*>(a.out) + row * a.ni + t.i0 + 32 * q, a.ni, nc, features, lane);
             }
           }
         }
@@ -827,9 +976,10 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (kPair) pair_sync();  // the other CTA reads this one's stages and arrives on its barriers until here
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    tmem_dealloc<kPair>(tmem);
   }
   if (threadIdx.x == 0 && sm.gave_up) {
     routing.report(NVFP4_ERR_TIMEOUT);

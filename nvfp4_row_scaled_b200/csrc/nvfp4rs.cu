@@ -624,8 +624,8 @@ bool code_tensor_map(CUtensorMap* map, const void* data, int64_t rows, int64_t K
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tiles of a launch with `jt` J rows a tile: exact for host splits, an upper
-// bound for device routing.
+// Tiles of a launch with `it` I tiles a group and `jt` J rows a tile: exact for
+// host splits, an upper bound for device routing.
 int64_t product_tiles(const HostRouting& r, int64_t, int64_t nj, int64_t it, int64_t jt, bool wgrad) {
   int64_t n = 0;
   for (int32_t g = 0; g < r.E; g++) n += ((wgrad ? nj : r.off[g + 1] - r.off[g]) + jt - 1) / jt * it;
@@ -635,45 +635,78 @@ int64_t product_tiles(const DeviceRouting& r, int64_t rows, int64_t nj, int64_t 
   return wgrad ? r.E * ((nj + jt - 1) / jt) * it : (rows / jt + std::min<int64_t>(rows, r.E)) * it;
 }
 
+template <int kMode, bool kTma, bool kPair, class Routing>
+nvfp4_status start_gemm(const Routing& routing, const GemmArgs& a, int64_t i_rows, int64_t j_rows, int64_t tiles, int sms,
+                        cudaStream_t stream) {
+  CUtensorMap imap, jmap, jmap_small;
+  if (kTma) {
+    if (!code_tensor_map(&imap, a.i.data, i_rows, a.K, kGI) || !code_tensor_map(&jmap, a.j.data, j_rows, a.K, kGBigJ) ||
+        !code_tensor_map(&jmap_small, a.j.data, j_rows, a.K, kGBoxJ))
+      return NVFP4_ERR_CUDA;
+  } else {
+    std::memset(&imap, 0, sizeof(imap));
+    std::memset(&jmap, 0, sizeof(jmap));
+    std::memset(&jmap_small, 0, sizeof(jmap_small));
+  }
+  auto kernel = group_gemm_kernel<Routing, kMode, kTma, kPair>;
+  constexpr bool kGated = kMode == kGemmGated;
+  const size_t smem = gemm_smem_bytes<kGated>(routing.E) + 1024;  // + room to align the block to 1024 bytes
+  static_assert(gemm_smem_bytes<kGated>(NVFP4_MAX_GROUPS) + 1024 <= 227 * 1024, "product kernel shared memory");
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return NVFP4_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  const int64_t grid = kPair ? 2 * std::min<int64_t>(tiles, sms / 2) : std::min<int64_t>(tiles, sms);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kGThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  // the adapters' first half is the kernel before this one: its result is
+  // waited for in the epilogue only
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (kMode == kGemmAdapter) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (kPair) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = 2;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, routing, imap, jmap, jmap_small, a));
+}
+
 // `i_rows`, `j_rows`: rows of the two stacked operands (for the tensor maps and
 // the debug build's ranges); a: everything but jt, loaders, producer.
 template <int kMode, class Routing>
 nvfp4_status launch_gemm(const Routing& routing, GemmArgs a, int64_t rows, int64_t i_rows, int64_t j_rows,
                          cudaStream_t stream) {
   constexpr bool kWgrad = kMode == kGemmWgrad;
-  const int32_t E = routing.E;
-  const int64_t it = (a.ni + kGI - 1) / kGI;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  // J rows of a tile: the most that fit, halved while there are fewer tiles than SMs
-  const int jt_least = a.j.tiled ? 128 : 32;
-  a.jt = kMode == kGemmGated ? kGJ / 2 : kGJ;
-  int64_t tiles = product_tiles(routing, rows, a.nj, it, a.jt, kWgrad);
-  while (a.jt > jt_least && tiles < sms) {
-    a.jt /= 2;
-    tiles = product_tiles(routing, rows, a.nj, it, a.jt, kWgrad);
+  // pairs of CTAs where their tiles fill the GPU, else one CTA a tile, its J rows
+  // halved while there are fewer tiles than SMs
+  const int64_t it1 = (a.ni + kGI - 1) / kGI, it2 = (a.ni + 2 * kGI - 1) / (2 * kGI);
+  a.jt = 2 * GemmStage<kMode == kGemmGated>::kJRows;
+  int64_t tiles = product_tiles(routing, rows, a.nj, it2, a.jt, kWgrad);
+  const bool pair = tiles >= sms / 2;
+  if (!pair) {
+    do {
+      a.jt /= 2;
+      tiles = product_tiles(routing, rows, a.nj, it1, a.jt, kWgrad);
+    } while (a.jt > 32 && tiles < sms);
   }
   if (tiles == 0) return NVFP4_OK;
   if (tiles > INT32_MAX) return NVFP4_ERR_UNSUPPORTED;
   const bool tma = !kWgrad && a.K % 32 == 0 && a.K > 0;
-  a.loaders = !tma || !a.i.tiled || !a.j.tiled;
-  a.producer = tma || a.i.tiled || a.j.tiled;
-  CUtensorMap imap, jmap, jmap_small;
-  std::memset(&imap, 0, sizeof(imap));
-  std::memset(&jmap, 0, sizeof(jmap));
-  std::memset(&jmap_small, 0, sizeof(jmap_small));
-  if (tma && (!code_tensor_map(&imap, a.i.data, i_rows, a.K, kGI) ||
-              !code_tensor_map(&jmap, a.j.data, j_rows, a.K, kGBigJ) ||
-              !code_tensor_map(&jmap_small, a.j.data, j_rows, a.K, kGBoxJ)))
-    return NVFP4_ERR_CUDA;
-  auto kernel = group_gemm_kernel<Routing, kMode, !kWgrad>;
-  if (!tma) kernel = group_gemm_kernel<Routing, kMode, false>;
-  const size_t smem = gemm_smem_bytes(E) + 1024;  // + room to align the block to 1024 bytes
-  static_assert(gemm_smem_bytes(NVFP4_MAX_GROUPS) + 1024 <= 227 * 1024, "product kernel shared memory");
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-    return NVFP4_ERR_CUDA;
+  a.jbulk = a.j.tiled && a.jt % kRows == 0;
+  a.loaders = !tma || !a.i.tiled || !a.jbulk;
+  a.producer = tma || a.i.tiled || a.jbulk;
 #ifdef NVFP4_CHECK_BOUNDS
   {
     const size_t in = static_cast<size_t>(i_rows) * (kWgrad ? 0 : a.K), jn = static_cast<size_t>(j_rows) * (kWgrad ? 0 : a.K);
@@ -696,19 +729,13 @@ nvfp4_status launch_gemm(const Routing& routing, GemmArgs a, int64_t rows, int64
                     .set(stream));
   }
 #endif
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, sms)));
-  cfg.blockDim = dim3(kGThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  // the adapters' first half is the kernel before this one: its result is
-  // waited for in the epilogue only
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = kMode == kGemmAdapter ? 1 : 0;
-  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, routing, imap, jmap, jmap_small, a));
+  if (tma) {
+    constexpr bool kT = !kWgrad;
+    return pair ? start_gemm<kMode, kT, true>(routing, a, i_rows, j_rows, tiles, sms, stream)
+                : start_gemm<kMode, kT, false>(routing, a, i_rows, j_rows, tiles, sms, stream);
+  }
+  return pair ? start_gemm<kMode, false, true>(routing, a, i_rows, j_rows, tiles, sms, stream)
+              : start_gemm<kMode, false, false>(routing, a, i_rows, j_rows, tiles, sms, stream);
 }
 
 GemmOperand operand(const nvfp4_matrix* m) {
