@@ -106,7 +106,8 @@ struct GemmArgs {
   int32_t ni;        // output columns: I rows of a group (gated: of each half)
   int32_t nj;        // wgrad: J rows of a group
   int32_t K;         // contraction (wgrad: the group's rows instead)
-  int32_t jt;        // J rows of a tile: 32, 64, 128 or 256
+  int32_t jt, jt_log;       // J rows of a tile: 32, 64, 128 or 256; its logarithm
+  uint32_t it, it_magic;    // I tiles of a group; floor(2^32 / it), 2^32 - 1 for it = 1
   int32_t jbulk;     // nonzero: J scales by bulk copies (tiled, and J tiles of whole 128-row blocks)
   int32_t loaders;   // nonzero: warps 2-5 take part
   int32_t producer;  // nonzero: warp 0 takes part
@@ -291,34 +292,42 @@ struct GemmTile {
   int64_t goff;     // wgrad: the group's first routed row
 };
 
-// Forward-only walk: seek(t) for increasing t.
+// The tiles of a CTA, one after the other: index first(), first() + step(), ...
+// over the groups' tiles in order. Every role walks them for itself, so a step
+// costs no integer division: jt is a power of two, and the I tiles of a group are
+// divided out with a reciprocal (a.it_magic = floor(2^32 / it), one short at most).
 template <int kMode, bool kPair>
 struct GemmWalk {
+  static constexpr int kI = kPair ? 2 * kGI : kGI;  // I rows of a tile
   const RoutingSmem& rs;
   const GemmArgs& a;
-  static constexpr int kI = kPair ? 2 * kGI : kGI;  // I rows of a tile
-  int32_t g = 0;
-  int64_t before = 0;  // tiles of the groups before g
-  // tile indices: first() and then every step()-th; both CTAs of a pair take the same
-  __device__ __forceinline__ int64_t first() const { return kPair ? blockIdx.x >> 1 : blockIdx.x; }
-  __device__ __forceinline__ int64_t step() const { return kPair ? gridDim.x >> 1 : gridDim.x; }
-  __device__ __forceinline__ GemmWalk(const RoutingSmem& r, const GemmArgs& x) : rs(r), a(x) {}
+  int32_t g = -1;          // group of the last tile found,
+  int32_t row = 0, m = 0;  // its first routed row and its rows
+  uint32_t t;              // next tile index
+  uint32_t before = 0, end = 0;  // tile indices of group g
+  __device__ __forceinline__ GemmWalk(const RoutingSmem& r, const GemmArgs& x) : rs(r), a(x) {
+    t = kPair ? blockIdx.x >> 1 : blockIdx.x;  // both CTAs of a pair take the same
+  }
 
-  __device__ __forceinline__ bool seek(int64_t t, GemmTile& tile) {
-    const int32_t it = (a.ni + kI - 1) / kI;
-    int32_t m = 0;
-    for (; g < rs.E; g++) {
-      m = rs.off[g + 1] - rs.off[g];
-      const int64_t n = static_cast<int64_t>(((kMode == kGemmWgrad ? a.nj : m) + a.jt - 1) / a.jt) * it;
-      if (t < before + n) break;
-      before += n;
+  __device__ __forceinline__ bool next(GemmTile& tile) {
+    while (t >= end) {
+      if (++g >= rs.E) return false;
+      row = rs.off[g];
+      m = rs.off[g + 1] - row;
+      before = end;
+      end += static_cast<uint32_t>(((kMode == kGemmWgrad ? a.nj : m) + a.jt - 1) >> a.jt_log) * a.it;
     }
-    if (g >= rs.E) return false;
-    const int32_t local = static_cast<int32_t>(t - before);
-    const int32_t jb = local / it, ib = local - jb * it;
+    const uint32_t local = t - before;
+    t += kPair ? gridDim.x >> 1 : gridDim.x;
+    uint32_t jb = __umulhi(local, a.it_magic);
+    uint32_t ib = local - jb * a.it;
+    if (ib >= a.it) {
+      jb++;
+      ib -= a.it;
+    }
     const int32_t jn = kMode == kGemmWgrad ? a.nj : m;
     tile.kc = kMode == kGemmWgrad ? m : a.K;
-    tile.i0 = ib * kI;
+    tile.i0 = static_cast<int32_t>(ib) * kI;
     tile.iv = min(kGI, a.ni - tile.i0);
     if (kPair && (blockIdx.x & 1)) {
       // the second CTA's rows; with none left it works on the first's again and stores nothing
@@ -326,13 +335,25 @@ struct GemmWalk {
       tile.iv = max(0, min(kGI, left));
       if (left > 0) tile.i0 += kGI;
     }
-    tile.j0 = jb * a.jt;
+    tile.j0 = static_cast<int32_t>(jb << a.jt_log);
     tile.jv = min(a.jt, jn - tile.j0);
-    tile.goff = rs.off[g];
-    const int64_t in = kMode == kGemmGated ? int64_t{2} * a.ni : a.ni;
-    tile.irow = g * in + tile.i0;
-    tile.jrow = (kMode == kGemmWgrad ? static_cast<int64_t>(g) * a.nj : tile.goff) + tile.j0;
+    tile.goff = row;
+    const int32_t in = kMode == kGemmGated ? 2 * a.ni : a.ni;
+    tile.irow = static_cast<int64_t>(g) * in + tile.i0;
+    tile.jrow = (kMode == kGemmWgrad ? static_cast<int64_t>(g) * a.nj : row) + tile.j0;
     return true;
+  }
+};
+
+// Position in the ring of stages.
+template <int kStages>
+struct GemmRing {
+  uint32_t s = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == kStages) {
+      s = 0;
+      phase ^= 1;
+    }
   }
 };
 
@@ -341,12 +362,11 @@ template <int kMode, bool kPair>
 struct GemmBlocks {
   GemmWalk<kMode, kPair> walk;
   GemmTile t;
-  int64_t ti;
   int32_t kb, nkb;
   bool more;
-  __device__ __forceinline__ GemmBlocks(const RoutingSmem& r, const GemmArgs& x) : walk(r, x), ti(walk.first()), kb(0) { tile(); }
+  __device__ __forceinline__ GemmBlocks(const RoutingSmem& r, const GemmArgs& x) : walk(r, x), kb(0) { tile(); }
   __device__ __forceinline__ void tile() {
-    for (; (more = walk.seek(ti, t)); ti += walk.step()) {
+    while ((more = walk.next(t))) {
       nkb = (t.kc + kGK - 1) / kGK;
       if (nkb > 0) return;
     }
@@ -354,7 +374,6 @@ struct GemmBlocks {
   __device__ __forceinline__ void next() {
     if (++kb < nkb) return;
     kb = 0;
-    ti += walk.step();
     tile();
   }
 };
@@ -596,10 +615,11 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
       Walk walk(sm.routing, a);
       GemmTile t;
       const bool elected = elect_one();
+      GemmRing<kStages> ring;
       uint32_t n = 0;
       bool ok = true;
       const uint64_t pol = policy_evict_normal();
-      for (int64_t ti = walk.first(); ok && walk.seek(ti, t); ti += walk.step()) {
+      while (ok && walk.next(t)) {
         const int nkb = (t.kc + kGK - 1) / kGK;
         // this CTA's J rows: boxes of 128, the rest in boxes of 32
         const int jrows = kPair ? ((t.jv + 31) & ~31) / 2 : t.jv;
@@ -616,9 +636,9 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
         if (kTma) data_bytes = (kGated ? 2 : 1) * kGIBytes + (big * kGBigJ + small * kGBoxJ) * 128;
         if (a.i.tiled) tiles += kGated ? 2 : 1;
         if (a.jbulk) tiles += jblocks;
-        for (int kb = 0; kb < nkb; kb++, n++) {
-          const int s = n % kStages;
-          if (!mbar_wait(&sm.empty[s], ((n / kStages) & 1) ^ 1)) {
+        for (int kb = 0; kb < nkb; kb++, n++, ring.next()) {
+          const uint32_t s = ring.s;
+          if (!mbar_wait(&sm.empty[s], ring.phase ^ 1)) {
             ok = false;
             break;
           }
@@ -658,23 +678,24 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
       // second CTA of a pair: tells the first that a stage is full
       GemmBlocks<kMode, kPair> at(sm.routing, a);
       const bool elected = elect_one();
-      for (uint32_t n = 0; at.more; at.next(), n++) {
-        const int s = n % kStages;
-        if (!mbar_wait(&sm.full[s], (n / kStages) & 1)) {
+      GemmRing<kStages> ring;
+      for (; at.more; at.next(), ring.next()) {
+        if (!mbar_wait(&sm.full[ring.s], ring.phase)) {
           sm.gave_up = 1;
           break;
         }
-        if (elected) mbar_arrive_first(&sm.peer_full[s]);
+        if (elected) mbar_arrive_first(&sm.peer_full[ring.s]);
         __syncwarp();
       }
     } else if (warp == 1) {
       Walk walk(sm.routing, a);
       GemmTile t;
       const bool elected = elect_one();
-      uint32_t n = 0, tiles = 0;
+      GemmRing<kStages> ring;
+      uint32_t tiles = 0;
       bool ok = true;
       const uint32_t stages = smem_addr(sm.stage[0]);
-      for (int64_t ti = walk.first(); ok && walk.seek(ti, t); ti += walk.step()) {
+      while (ok && walk.next(t)) {
         const int nkb = (t.kc + kGK - 1) / kGK;
         if (nkb == 0) continue;
         if (tiles > 0 && !mbar_wait(&sm.acc_free, (tiles - 1) & 1)) {
@@ -685,10 +706,9 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
         const uint32_t acc = tmem + ((tiles & 1) ? kGAcc1 : 0);
         const int cols = kPair ? (t.jv + 31) & ~31 : (t.jv + 15) & ~15;
         const uint32_t idesc = mma_idesc<kPair>(cols);
-        for (int kb = 0; kb < nkb; kb++, n++) {
-          const int s = n % kStages;
-          if (!mbar_wait(&sm.full[s], (n / kStages) & 1) ||
-              (kPair && !mbar_wait(&sm.peer_full[s], (n / kStages) & 1))) {
+        for (int kb = 0; kb < nkb; kb++, ring.next()) {
+          const uint32_t s = ring.s;
+          if (!mbar_wait(&sm.full[s], ring.phase) || (kPair && !mbar_wait(&sm.peer_full[s], ring.phase))) {
             ok = false;
             break;
           }
@@ -718,6 +738,7 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
       const int tid = threadIdx.x - kGLoadWarp * 32;
       GemmBlocks<kMode, kPair> at(sm.routing, a);     // the block whose stage is filled
       GemmBlocks<kMode, kPair> ahead(sm.routing, a);  // the block whose scales are read, one further
+      GemmRing<kStages> ring;
       uint32_t n = 0;
       bool ok = true;
       // A thread's three rows of a stage's scales: row tid of each 128-row block
@@ -767,17 +788,16 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
         read(ahead, cur);
         ahead.next();
       }
-      for (; at.more; at.next(), n++) {
+      for (; at.more; at.next(), n++, ring.next()) {
         if (ahead.more) {
           read(ahead, nxt);
           ahead.next();
         }
-        const int s = n % kStages;
-        if (!mbar_wait(&sm.empty[s], ((n / kStages) & 1) ^ 1)) {
+        if (!mbar_wait(&sm.empty[ring.s], ring.phase ^ 1)) {
           ok = false;
           break;
         }
-        uint8_t* st = sm.stage[s];
+        uint8_t* st = sm.stage[ring.s];
         if (!kTma) {
           const GemmTile& t = at.t;
           const int64_t row_bytes = t.kc / 2;
@@ -856,8 +876,7 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
       GemmTile t, t1;
       Factors f{}, f1{};
       uint32_t tiles = 0;
-      int64_t ti = walk.first();
-      bool more = walk.seek(ti, t1);
+      bool more = walk.next(t1);
       if (more && t1.kc > 0) read(t1, 0, f1);
       float* sjw = sm.sj[warp - kGEpiWarp];
       uint32_t(&turn)[16][32] = sm.turn[warp - kGEpiWarp];
@@ -865,8 +884,7 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
         t = t1;
         f = f1;
         const bool empty = t.kc == 0;
-        ti += walk.step();
-        more = walk.seek(ti, t1);
+        more = walk.next(t1);
         f1 = Factors{};
         if (more && t1.kc > 0) read(t1, (tiles + (empty ? 0 : 1)) & 1, f1);
         const bool live = il < t.iv;

@@ -703,6 +703,10 @@ nvfp4_status launch_gemm(const Routing& routing, GemmArgs a, int64_t rows, int64
   }
   if (tiles == 0) return NVFP4_OK;
   if (tiles > INT32_MAX) return NVFP4_ERR_UNSUPPORTED;
+  a.jt_log = 0;
+  while ((1 << a.jt_log) < a.jt) a.jt_log++;
+  a.it = static_cast<uint32_t>(pair ? it2 : it1);
+  a.it_magic = a.it == 1 ? 0xFFFFFFFFu : static_cast<uint32_t>((uint64_t{1} << 32) / a.it);
   const bool tma = !kWgrad && a.K % 32 == 0 && a.K > 0;
   a.jbulk = a.j.tiled && a.jt % kRows == 0;
   a.loaders = !tma || !a.i.tiled || !a.jbulk;
