@@ -380,69 +380,77 @@ struct GemmBlocks {
 
 // ------------------------------------------------------------- loader roles
 
-// Row r of a k block's codes (kcopy: 16 or 8 bytes a copy) and its swizzled place.
+// A k block's codes of `rows` rows (`valid` of them real, the rest zeros), 128
+// bytes a row, kCopy bytes a copy, into the swizzled stage. The 128 threads cover
+// 128 / (128 / kCopy) rows at a time, a multiple of 8: a thread's place in the
+// swizzle pattern and its distance to the row's end stay the same, so a copy
+// costs three instructions.
 template <int kCopy>
 __device__ __forceinline__ void load_codes(uint32_t dst, const uint8_t* data, int64_t row_bytes, int rows, int valid,
                                            int32_t kbyte, int tid) {
-  constexpr int kPer = 128 / kCopy;
-  for (int c = tid; c < rows * kPer; c += 128) {
-    const int r = c / kPer, o = (c % kPer) * kCopy;
-    int n = 0;
-    const uint8_t* src = data;
-    if (r < valid) {
-      const int64_t at = static_cast<int64_t>(kbyte) + o;
-      n = static_cast<int>(min(static_cast<int64_t>(kCopy), max(row_bytes - at, int64_t{0})));
-      if (n > 0) src = data + r * row_bytes + at;
-    }
-    cp_async<kCopy>(dst + r * 128 + ((((o >> 4) ^ (r & 7)) << 4) | (o & 15)), src, n);
+  constexpr int kPer = 128 / kCopy, kStep = 128 / kPer;
+  const int r0 = tid / kPer, o = (tid % kPer) * kCopy;
+  const int64_t left = row_bytes - kbyte - o;
+  const int n = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(kCopy), left)));
+  const uint8_t* src = n > 0 ? data + r0 * row_bytes + kbyte + o : data;
+  const int64_t step = n > 0 ? kStep * row_bytes : 0;
+  uint32_t d = dst + r0 * 128 + ((((o >> 4) ^ (r0 & 7)) << 4) | (o & 15));
+#pragma unroll 8
+  for (int r = r0; r < rows; r += kStep) {
+    const bool in = r < valid;
+    cp_async<kCopy>(d, in ? src : data, in ? n : 0);
+    src += step;
+    d += kStep * 128;
   }
 }
 
-// The 16 block scales (one k block) of a row that has `left` scales from `src`
-// on, zeros behind its end. Wide loads where the rows' alignment allows: a
-// warp's 32 rows are 32 lines, and each load instruction pays for every line.
-__device__ __forceinline__ uint4 load_scale_row(const uint8_t* src, int32_t cols, int32_t left) {
-  if ((cols & 15) == 0) return gload(reinterpret_cast<const uint4*>(src));
-  uint32_t v[4];
-  if ((cols & 3) == 0) {
+// How a thread reads the 16 scales of a row and k block: one load where the rows
+// are 16-byte aligned (a warp's 32 rows are 32 lines, and every load instruction
+// pays for each), four words where they are 4-byte aligned, the five words
+// around them where rows start at any byte, four words 512 bytes apart out of
+// 128x4 tiles.
+enum ScaleRead : int { kRead16 = 0, kReadWords = 1, kReadBytes = 2, kReadTiled = 3 };
+
+// `left`: scales from p to the row's end. What is read raw is put together by
+// scale_words() later, so that a read is not waited for here. A stacked matrix
+// ends on a 16-byte boundary: a word that holds a byte of it lies inside it.
+__device__ __forceinline__ void read_scales(const uint8_t* p, int how, int32_t left, uint32_t (&w)[5]) {
 #pragma unroll
-    for (int k = 0; k < 4; k++) v[k] = 4 * k < left ? gload(reinterpret_cast<const uint32_t*>(src) + k) : 0u;
+  for (int k = 0; k < 5; k++) w[k] = 0u;
+  if (p == nullptr) return;
+  if (how == kRead16) {
+    const uint4 v = gload(reinterpret_cast<const uint4*>(p));
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  } else if (how == kReadBytes) {
+    const int b = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 3);
+#pragma unroll
+    for (int k = 0; k < 5; k++)
+      if (4 * k < left + b) w[k] = gload(reinterpret_cast<const uint32_t*>(p - b) + k);
   } else {
-    // rows start at any byte: the aligned words around the 16 bytes, shifted. A
-    // stacked matrix ends on a 16-byte boundary, so a word that holds a byte of
-    // it lies inside it.
-    const uint32_t sh = (reinterpret_cast<uintptr_t>(src) & 3) * 8;
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(src - (sh >> 3));
-    uint32_t w[5];
+    const int step = how == kReadTiled ? kGScaleTile / 4 : 1;
 #pragma unroll
-    for (int k = 0; k < 5; k++) w[k] = 4 * k < left + static_cast<int>(sh >> 3) ? gload(p + k) : 0u;
-#pragma unroll
-    for (int k = 0; k < 4; k++) {
-      v[k] = __funnelshift_r(w[k], w[k + 1], sh);
-      const int n = left - 4 * k;
-      if (n < 4) v[k] = n <= 0 ? 0u : v[k] & (0xFFFFFFFFu >> (8 * (4 - n)));
-    }
+    for (int k = 0; k < 4; k++)
+      if (4 * k < left) w[k] = gload(reinterpret_cast<const uint32_t*>(p) + k * step);
   }
-  return make_uint4(v[0], v[1], v[2], v[3]);
 }
-
-// The same of row r of a 128-row block of 128x4 tiles (`left` a multiple of 4).
-__device__ __forceinline__ uint4 load_tiled_row(const uint8_t* block, int r, int32_t left) {
-  const uint8_t* p = block + (r & 31) * 16 + (r >> 5) * 4;
-  uint32_t v[4];
+// shift: bits from the first word's start to the first scale (kReadBytes)
+__device__ __forceinline__ void scale_words(uint32_t shift, int32_t left, uint32_t (&w)[5]) {
 #pragma unroll
-  for (int k = 0; k < 4; k++) v[k] = 4 * k < left ? gload(reinterpret_cast<const uint32_t*>(p + k * kGScaleTile)) : 0u;
-  return make_uint4(v[0], v[1], v[2], v[3]);
+  for (int k = 0; k < 4; k++) {
+    w[k] = __funnelshift_r(w[k], w[k + 1], shift);
+    const int n = left - 4 * k;
+    if (n < 4) w[k] = n <= 0 ? 0u : w[k] & (0xFFFFFFFFu >> (8 * (4 - n)));
+  }
 }
-
 // Row r's 16 scales of a k block into 128x4 tiles: scale (r, 4 k + b) at tile k
 // of the 128-row block, byte (r % 32) * 16 + (r / 32) * 4 + b.
-__device__ __forceinline__ void store_scale_row(uint8_t* dst, int r, const uint4& v) {
+__device__ __forceinline__ void store_scales_row(uint8_t* dst, int r, const uint32_t (&w)[5]) {
   uint8_t* d = dst + (r & 31) * 16 + (r >> 5) * 4;
-  *reinterpret_cast<uint32_t*>(d) = v.x;
-  *reinterpret_cast<uint32_t*>(d + kGScaleTile) = v.y;
-  *reinterpret_cast<uint32_t*>(d + 2 * kGScaleTile) = v.z;
-  *reinterpret_cast<uint32_t*>(d + 3 * kGScaleTile) = v.w;
+#pragma unroll
+  for (int k = 0; k < 4; k++) *reinterpret_cast<uint32_t*>(d + k * kGScaleTile) = w[k];
 }
 
 __device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
@@ -742,41 +750,53 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
       uint32_t n = 0;
       bool ok = true;
       // A thread's three rows of a stage's scales: row tid of each 128-row block
-      // (I, then two of J; gated: gate, up, J).
+      // (I, then two of J; gated: gate, up, J); p: where the next block's lie.
+      constexpr int kJ = kGated ? 2 : 1;
       struct Rows {
-        uint4 v[3];
+        uint32_t w[3][5];
+        int32_t left;
+        uint32_t shift;  // bits, a byte for each row
       };
-      auto read = [&](GemmBlocks<kMode, kPair>& b, Rows& r) {
-        const GemmTile& t = b.t;
-        const int32_t cols = t.kc / 16, first = b.kb * 16, left = cols - first;
-        const uint8_t *is, *js;
-        if (kMode == kGemmWgrad) {
-          is = a.i.scale + t.goff * a.ni / 16 + static_cast<int64_t>(t.i0) * cols;
-          js = a.j.scale + t.goff * a.nj / 16 + static_cast<int64_t>(t.j0) * cols;
-        } else {
-          is = a.i.scale + t.irow * cols;
-          js = a.j.scale + t.jrow * cols;
-        }
-        is += static_cast<int64_t>(tid) * cols + first;
-        js += static_cast<int64_t>(tid) * cols + first;
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        constexpr int kJ = kGated ? 2 : 1;
-        r.v[0] = !a.i.tiled && tid < t.iv ? load_scale_row(is, cols, left) : zero;
-        if (kGated)
-          r.v[1] = !a.i.tiled && tid < t.iv ? load_scale_row(is + static_cast<int64_t>(a.ni) * cols, cols, left) : zero;
-        if (a.j.tiled) {
+      const uint8_t* p[3] = {nullptr, nullptr, nullptr};
+      int how = kRead16, jhow = kRead16;
+      auto start = [&](const GemmTile& t) {
+        const int32_t cols = t.kc / 16;
+        how = (cols & 15) == 0 ? kRead16 : (cols & 3) == 0 ? kReadWords : kReadBytes;
+        jhow = a.j.tiled ? kReadTiled : how;
+        const int64_t ib = kMode == kGemmWgrad ? t.goff * a.ni / 16 + static_cast<int64_t>(t.i0) * cols : t.irow * cols;
+        const int64_t jb = kMode == kGemmWgrad ? t.goff * a.nj / 16 : (t.jrow - t.j0) * cols;  // the group's first row
+        p[0] = !a.i.tiled && tid < t.iv ? a.i.scale + ib + static_cast<int64_t>(tid) * cols : nullptr;
+        if (kGated) p[1] = p[0] != nullptr ? p[0] + static_cast<int64_t>(a.ni) * cols : nullptr;
+        if (!a.j.tiled) {
+          const uint8_t* js = a.j.scale + jb + static_cast<int64_t>(t.j0 + tid) * cols;
+          p[kJ] = tid < t.jv ? js : nullptr;
+          if (!kGated) p[2] = tid + 128 < t.jv ? js + static_cast<int64_t>(128) * cols : nullptr;
+        } else if (!a.jbulk) {
           // a J tile inside a 128-row block (jt < 128): its rows out of the block's
-          // tiles. The scales in tensor memory cannot start at a later column.
-          if (!a.jbulk) {
-            const int64_t kt = t.kc / 64;
-            const uint8_t* tb = a.j.scale + (kMode == kGemmWgrad ? t.goff * a.nj / 16 + t.j0 / 128 * kt * kGScaleTile
-                                                                 : t.jrow / 128 * kt * kGScaleTile);
-            r.v[kJ] = tid < t.jv ? load_tiled_row(tb + b.kb * 4 * kGScaleTile, (t.j0 & 127) + tid, left) : zero;
-          }
-        } else {
-          r.v[kJ] = tid < t.jv ? load_scale_row(js, cols, left) : zero;
-          if (!kGated) r.v[2] = tid + 128 < t.jv ? load_scale_row(js + static_cast<int64_t>(128) * cols, cols, left) : zero;
+          // tiles; the scales in tensor memory cannot start at a later column
+          const int r = (t.j0 & 127) + tid;
+          p[kJ] = tid < t.jv ? a.j.scale + jb + static_cast<int64_t>(t.j0 >> 7) * (cols >> 2) * kGScaleTile + (r & 31) * 16 +
+                                   (r >> 5) * 4
+                             : nullptr;
         }
+      };
+      auto read = [&](const GemmBlocks<kMode, kPair>& b, Rows& r) {
+        if (b.kb == 0) start(b.t);
+        r.left = b.t.kc / 16 - b.kb * 16;
+        r.shift = 0;
+#pragma unroll
+        for (int k = 0; k < 3; k++) {
+          const int h = k == kJ ? jhow : how;
+          read_scales(p[k], h, r.left, r.w[k]);
+          if (p[k] != nullptr) {
+            if (h == kReadBytes) r.shift |= static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p[k]) & 3) << (8 * k + 3);
+            p[k] += h == kReadTiled ? 4 * kGScaleTile : 16;
+          }
+        }
+      };
+      auto store = [&](uint8_t* dst, int k, Rows& r, bool tiled) {
+        if (!tiled) scale_words((r.shift >> (8 * k)) & 0xFF, r.left, r.w[k]);
+        store_scales_row(dst, tid, r.w[k]);
       };
       auto publish = [&](uint32_t k) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -813,7 +833,7 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
           // this CTA's J rows
           const int cols = kPair ? ((t.jv + 31) & ~31) / 2 : (t.jv + 15) & ~15, kbyte = at.kb * 128;
           const int jv = max(0, min(cols, t.jv - rank * cols));
-          jc += rank * cols * row_bytes;
+          if (jv > 0) jc += rank * cols * row_bytes;
           if (row_bytes % 16 == 0) {
             load_codes<16>(d, ic, row_bytes, kGI, t.iv, kbyte, tid);
             if (kGated) load_codes<16>(d + kGIBytes, ic + a.ni * row_bytes, row_bytes, kGI, t.iv, kbyte, tid);
@@ -827,12 +847,12 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
         }
         uint8_t* sf = st + Stage::kData;
         if (!a.i.tiled) {
-          store_scale_row(sf, tid, cur.v[0]);
-          if (kGated) store_scale_row(sf + 4 * kGScaleTile, tid, cur.v[1]);
+          store(sf, 0, cur, false);
+          if (kGated) store(sf + 4 * kGScaleTile, 1, cur, false);
         }
         if (!a.jbulk) {
-          store_scale_row(sf + Stage::kISf, tid, cur.v[kGated ? 2 : 1]);
-          if (!kGated && at.t.jv > 128) store_scale_row(sf + Stage::kISf + 4 * kGScaleTile, tid, cur.v[2]);
+          store(sf + Stage::kISf, kJ, cur, a.j.tiled);
+          if (!kGated && at.t.jv > 128) store(sf + Stage::kISf + 4 * kGScaleTile, 2, cur, a.j.tiled);
         }
         cur = nxt;
         if (kTma) {
@@ -843,7 +863,8 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
         }
       }
       cp_async_wait<0>();
-      if (!ok) sm.gave_up = 1;
+      if (!ok)
+        sm.gave_up = 1;
       else if (!kTma)
         for (uint32_t k = n > kGLoadLag ? n - kGLoadLag : 0; k < n; k++) publish(k);
     } else if (warp >= kGEpiWarp) {
