@@ -41,11 +41,11 @@
 //   warp 1      tensor memory, scale copies shared -> tensor memory, MMAs (in
 //               a pair the first CTA's; the second's passes on that its stage
 //               has been filled)
-//   warps 2-5   what TMA cannot address: row-major block scales (16 bytes a row
-//               and k block, read one block ahead into registers and written
-//               as the 128x4 tiles the MMA wants) and, with kTma = false, the
-//               codes themselves (row strides that are not multiples of 16
-//               bytes; wgrad's per-group strides)
+//   warps 2-5   what TMA cannot address, a stage to a warp: row-major block
+//               scales (16 bytes a row and k block, read ahead into registers
+//               and written as the 128x4 tiles the MMA wants) and, with kTma =
+//               false, the codes themselves (row strides that are not
+//               multiples of 16 bytes; wgrad's per-group strides)
 //   warps 6-13  epilogue: two warps for each 32-lane quarter, alternate
 //               32-column chunks
 // Tensor memory holds two 256-column accumulators at columns 0 and 192 that
@@ -81,7 +81,6 @@ constexpr int kGScaleTile = 512;     // 128 rows x 4 scales
 constexpr int kGSfBytes = 3 * 4 * kGScaleTile;  // I and two blocks of 128 J rows (gated: gate, up, J), 4 k steps
 constexpr int kGAcc1 = 192;          // first column of the second accumulator
 constexpr int kGSfCol = 448;         // first scale column
-constexpr int kGLoadLag = 2;         // loader stages in flight before the oldest is published
 
 // A stage: I codes (gated: gate, then up), the CTA's J codes, scales.
 template <bool kGated>
@@ -92,6 +91,7 @@ struct GemmStage {
   static constexpr int kISf = (kGated ? 2 : 1) * 4 * kGScaleTile;
   static constexpr int kBytes = kData + kGSfBytes;
   static constexpr int kStages = kGated ? 4 : 5;
+  static_assert(kStages >= 4, "four loader warps, a stage each");
 };
 
 struct GemmOperand {
@@ -380,27 +380,33 @@ struct GemmBlocks {
 
 // ------------------------------------------------------------- loader roles
 
-// A k block's codes of `rows` rows (`valid` of them real, the rest zeros), 128
-// bytes a row, kCopy bytes a copy, into the swizzled stage. The 128 threads cover
-// 128 / (128 / kCopy) rows at a time, a multiple of 8: a thread's place in the
-// swizzle pattern and its distance to the row's end stay the same, so a copy
-// costs three instructions.
+// A k block's codes of `rows` rows (`valid` of them real, the rest zeros; rows a
+// multiple of 8), 128 bytes a row, kCopy bytes a copy, into the swizzled stage, by
+// one warp. Eight rows at a time: a lane's places in the swizzle pattern and its
+// distance to the rows' ends stay the same, so a copy costs three instructions.
 template <int kCopy>
 __device__ __forceinline__ void load_codes(uint32_t dst, const uint8_t* data, int64_t row_bytes, int rows, int valid,
-                                           int32_t kbyte, int tid) {
-  constexpr int kPer = 128 / kCopy, kStep = 128 / kPer;
-  const int r0 = tid / kPer, o = (tid % kPer) * kCopy;
+                                           int32_t kbyte, int lane) {
+  constexpr int kPer = 128 / kCopy, kRows = 32 / kPer, kSteps = 8 / kRows;
+  const int r0 = lane / kPer, o = (lane % kPer) * kCopy;
   const int64_t left = row_bytes - kbyte - o;
   const int n = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(kCopy), left)));
   const uint8_t* src = n > 0 ? data + r0 * row_bytes + kbyte + o : data;
-  const int64_t step = n > 0 ? kStep * row_bytes : 0;
-  uint32_t d = dst + r0 * 128 + ((((o >> 4) ^ (r0 & 7)) << 4) | (o & 15));
-#pragma unroll 8
-  for (int r = r0; r < rows; r += kStep) {
-    const bool in = r < valid;
-    cp_async<kCopy>(d, in ? src : data, in ? n : 0);
-    src += step;
-    d += kStep * 128;
+  const int64_t step = n > 0 ? kRows * row_bytes : 0;
+  uint32_t d[kSteps];
+#pragma unroll
+  for (int i = 0; i < kSteps; i++) {
+    const int r = r0 + i * kRows;
+    d[i] = dst + r * 128 + ((((o >> 4) ^ r) << 4) | (o & 15));
+  }
+#pragma unroll 2
+  for (int rb = 0; rb < rows; rb += 8) {
+#pragma unroll
+    for (int i = 0; i < kSteps; i++) {
+      const bool in = rb + r0 + i * kRows < valid;
+      cp_async<kCopy>(d[i] + rb * 128, in ? src : data, in ? n : 0);
+      src += step;
+    }
   }
 }
 
@@ -445,12 +451,12 @@ __device__ __forceinline__ void scale_words(uint32_t shift, int32_t left, uint32
     if (n < 4) w[k] = n <= 0 ? 0u : w[k] & (0xFFFFFFFFu >> (8 * (4 - n)));
   }
 }
-// Row r's 16 scales of a k block into 128x4 tiles: scale (r, 4 k + b) at tile k
-// of the 128-row block, byte (r % 32) * 16 + (r / 32) * 4 + b.
-__device__ __forceinline__ void store_scales_row(uint8_t* dst, int r, const uint32_t (&w)[5]) {
-  uint8_t* d = dst + (r & 31) * 16 + (r >> 5) * 4;
+// The 16 scales each of rows lane, lane + 32, lane + 64 and lane + 96 of a 128-row
+// block into 128x4 tiles: scale (r, 4 k + b) at tile k, byte (r % 32) * 16 + (r / 32) * 4 + b.
+__device__ __forceinline__ void store_scales(uint8_t* dst, int lane, const uint32_t (&w)[4][5]) {
 #pragma unroll
-  for (int k = 0; k < 4; k++) *reinterpret_cast<uint32_t*>(d + k * kGScaleTile) = w[k];
+  for (int k = 0; k < 4; k++)
+    *reinterpret_cast<uint4*>(dst + k * kGScaleTile + lane * 16) = make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
 }
 
 __device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
@@ -599,7 +605,7 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; s++) {
-      mbar_init(&sm.full[s], (a.producer ? 1 : 0) + (a.loaders ? 4 : 0));
+      mbar_init(&sm.full[s], (a.producer ? 1 : 0) + (a.loaders ? 1 : 0));
       mbar_init(&sm.peer_full[s], 1);
       mbar_init(&sm.empty[s], 1);
     }
@@ -743,83 +749,80 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
         mbar_wait(&sm.drain, 0);
       }
     } else if (warp >= kGLoadWarp && warp < kGEpiWarp && a.loaders) {
-      const int tid = threadIdx.x - kGLoadWarp * 32;
-      GemmBlocks<kMode, kPair> at(sm.routing, a);     // the block whose stage is filled
-      GemmBlocks<kMode, kPair> ahead(sm.routing, a);  // the block whose scales are read, one further
+      // Each of the four warps fills every fourth stage by itself, so that four
+      // stages' latencies overlap.
+      GemmBlocks<kMode, kPair> at(sm.routing, a);
       GemmRing<kStages> ring;
-      uint32_t n = 0;
       bool ok = true;
-      // A thread's three rows of a stage's scales: row tid of each 128-row block
-      // (I, then two of J; gated: gate, up, J); p: where the next block's lie.
+      // Rows lane + 32 e of each 128-row block of scales (I, then two of J; gated:
+      // gate, up, J), read ahead as they are; p: the next block's, row lane.
       constexpr int kJ = kGated ? 2 : 1;
       struct Rows {
-        uint32_t w[3][5];
-        int32_t left;
-        uint32_t shift;  // bits, a byte for each row
+        uint32_t w[3][4][5];
       };
-      const uint8_t* p[3] = {nullptr, nullptr, nullptr};
-      int how = kRead16, jhow = kRead16;
-      auto start = [&](const GemmTile& t) {
-        const int32_t cols = t.kc / 16;
-        how = (cols & 15) == 0 ? kRead16 : (cols & 3) == 0 ? kReadWords : kReadBytes;
-        jhow = a.j.tiled ? kReadTiled : how;
-        const int64_t ib = kMode == kGemmWgrad ? t.goff * a.ni / 16 + static_cast<int64_t>(t.i0) * cols : t.irow * cols;
-        const int64_t jb = kMode == kGemmWgrad ? t.goff * a.nj / 16 : (t.jrow - t.j0) * cols;  // the group's first row
-        p[0] = !a.i.tiled && tid < t.iv ? a.i.scale + ib + static_cast<int64_t>(tid) * cols : nullptr;
-        if (kGated) p[1] = p[0] != nullptr ? p[0] + static_cast<int64_t>(a.ni) * cols : nullptr;
-        if (!a.j.tiled) {
-          const uint8_t* js = a.j.scale + jb + static_cast<int64_t>(t.j0 + tid) * cols;
-          p[kJ] = tid < t.jv ? js : nullptr;
-          if (!kGated) p[2] = tid + 128 < t.jv ? js + static_cast<int64_t>(128) * cols : nullptr;
-        } else if (!a.jbulk) {
-          // a J tile inside a 128-row block (jt < 128): its rows out of the block's
-          // tiles; the scales in tensor memory cannot start at a later column
-          const int r = (t.j0 & 127) + tid;
-          p[kJ] = tid < t.jv ? a.j.scale + jb + static_cast<int64_t>(t.j0 >> 7) * (cols >> 2) * kGScaleTile + (r & 31) * 16 +
-                                   (r >> 5) * 4
-                             : nullptr;
-        }
-      };
-      auto read = [&](const GemmBlocks<kMode, kPair>& b, Rows& r) {
-        if (b.kb == 0) start(b.t);
-        r.left = b.t.kc / 16 - b.kb * 16;
-        r.shift = 0;
+      Rows r;
+      auto read = [&] {
+        const GemmTile& t = at.t;
+        const int32_t cols = t.kc / 16, first = at.kb * 16, left = cols - first;
+        const int how = (cols & 15) == 0 ? kRead16 : (cols & 3) == 0 ? kReadWords : kReadBytes;
+        if (!a.i.tiled) {
+          const int64_t ib = kMode == kGemmWgrad ? t.goff * a.ni / 16 + static_cast<int64_t>(t.i0) * cols : t.irow * cols;
+          const uint8_t* p = a.i.scale + ib + static_cast<int64_t>(lane) * cols + first;
 #pragma unroll
-        for (int k = 0; k < 3; k++) {
-          const int h = k == kJ ? jhow : how;
-          read_scales(p[k], h, r.left, r.w[k]);
-          if (p[k] != nullptr) {
-            if (h == kReadBytes) r.shift |= static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p[k]) & 3) << (8 * k + 3);
-            p[k] += h == kReadTiled ? 4 * kGScaleTile : 16;
+          for (int e = 0; e < 4; e++) {
+            const bool in = lane + 32 * e < t.iv;
+            const uint8_t* pe = p + static_cast<int64_t>(32 * e) * cols;
+            read_scales(in ? pe : nullptr, how, left, r.w[0][e]);
+            if (kGated) read_scales(in ? pe + static_cast<int64_t>(a.ni) * cols : nullptr, how, left, r.w[1][e]);
+          }
+        }
+        if (!a.jbulk) {
+          const int64_t jb = kMode == kGemmWgrad ? t.goff * a.nj / 16 : (t.jrow - t.j0) * cols;  // the group's first row
+#pragma unroll
+          for (int h = 0; h < (kGated ? 1 : 2); h++) {
+            if (128 * h >= t.jv) break;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+              const int j = lane + 32 * e + 128 * h, jr = t.j0 + j;
+              const uint8_t* pe;
+              if (a.j.tiled)  // a J tile inside a 128-row block (jt < 128): its rows out of the block's tiles; the
+                              // scales in tensor memory cannot start at a later column
+                pe = a.j.scale + jb + (static_cast<int64_t>(jr >> 7) * (cols >> 2) + at.kb * 4) * kGScaleTile +
+                     (jr & 31) * 16 + ((jr & 127) >> 5) * 4;
+              else
+                pe = a.j.scale + jb + static_cast<int64_t>(jr) * cols + first;
+              read_scales(j < t.jv ? pe : nullptr, a.j.tiled ? kReadTiled : how, left, r.w[kJ + h][e]);
+            }
           }
         }
       };
-      auto store = [&](uint8_t* dst, int k, Rows& r, bool tiled) {
-        if (!tiled) scale_words((r.shift >> (8 * k)) & 0xFF, r.left, r.w[k]);
-        store_scales_row(dst, tid, r.w[k]);
+      // Words out of what was read raw: the rows' first bytes as read() found them.
+      auto words = [&](int k, int64_t row, bool tiled) {
+        const int32_t cols = at.t.kc / 16;
+        if (tiled || (cols & 15) == 0) return;
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+          scale_words((cols & 3) == 0 ? 0u : static_cast<uint32_t>((row + lane + 32 * e) * cols & 3) * 8, cols - at.kb * 16,
+                      r.w[k][e]);
       };
-      auto publish = [&](uint32_t k) {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.full[k % kStages]);
+      auto skip = [&](int n) {
+        for (int k = 0; k < n && at.more; k++) at.next();
       };
-      Rows cur, nxt;
-      if (ahead.more) {
-        read(ahead, cur);
-        ahead.next();
-      }
-      for (; at.more; at.next(), n++, ring.next()) {
-        if (ahead.more) {
-          read(ahead, nxt);
-          ahead.next();
-        }
-        if (!mbar_wait(&sm.empty[ring.s], ring.phase ^ 1)) {
+      const int mine = warp - kGLoadWarp;
+      skip(mine);
+      ring.s = mine;
+      if (at.more) read();
+      while (at.more) {
+        const uint32_t s = ring.s;
+        if (!mbar_wait(&sm.empty[s], ring.phase ^ 1)) {
           ok = false;
           break;
         }
-        uint8_t* st = sm.stage[ring.s];
+        uint8_t* st = sm.stage[s];
+        const GemmTile& t = at.t;
+        // the rows whose offsets decide the first byte (a group of wgrad starts on 16 bytes)
+        const int64_t i_row = kMode == kGemmWgrad ? t.i0 : t.irow, j_row = kMode == kGemmWgrad ? t.j0 : t.jrow;
         if (!kTma) {
-          const GemmTile& t = at.t;
           const int64_t row_bytes = t.kc / 2;
           const uint8_t *ic, *jc;
           if (kMode == kGemmWgrad) {
@@ -835,38 +838,47 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
           const int jv = max(0, min(cols, t.jv - rank * cols));
           if (jv > 0) jc += rank * cols * row_bytes;
           if (row_bytes % 16 == 0) {
-            load_codes<16>(d, ic, row_bytes, kGI, t.iv, kbyte, tid);
-            if (kGated) load_codes<16>(d + kGIBytes, ic + a.ni * row_bytes, row_bytes, kGI, t.iv, kbyte, tid);
-            load_codes<16>(d + Stage::kIData, jc, row_bytes, cols, jv, kbyte, tid);
+            load_codes<16>(d, ic, row_bytes, kGI, t.iv, kbyte, lane);
+            if (kGated) load_codes<16>(d + kGIBytes, ic + a.ni * row_bytes, row_bytes, kGI, t.iv, kbyte, lane);
+            load_codes<16>(d + Stage::kIData, jc, row_bytes, cols, jv, kbyte, lane);
           } else {
-            load_codes<8>(d, ic, row_bytes, kGI, t.iv, kbyte, tid);
-            if (kGated) load_codes<8>(d + kGIBytes, ic + a.ni * row_bytes, row_bytes, kGI, t.iv, kbyte, tid);
-            load_codes<8>(d + Stage::kIData, jc, row_bytes, cols, jv, kbyte, tid);
+            load_codes<8>(d, ic, row_bytes, kGI, t.iv, kbyte, lane);
+            if (kGated) load_codes<8>(d + kGIBytes, ic + a.ni * row_bytes, row_bytes, kGI, t.iv, kbyte, lane);
+            load_codes<8>(d + Stage::kIData, jc, row_bytes, cols, jv, kbyte, lane);
           }
           cp_async_commit();
         }
         uint8_t* sf = st + Stage::kData;
         if (!a.i.tiled) {
-          store(sf, 0, cur, false);
-          if (kGated) store(sf + 4 * kGScaleTile, 1, cur, false);
+          words(0, i_row, false);
+          store_scales(sf, lane, r.w[0]);
+          if (kGated) {
+            words(1, i_row + a.ni, false);
+            store_scales(sf + 4 * kGScaleTile, lane, r.w[1]);
+          }
         }
         if (!a.jbulk) {
-          store(sf + Stage::kISf, kJ, cur, a.j.tiled);
-          if (!kGated && at.t.jv > 128) store(sf + Stage::kISf + 4 * kGScaleTile, 2, cur, a.j.tiled);
+          words(kJ, j_row, a.j.tiled);
+          store_scales(sf + Stage::kISf, lane, r.w[kJ]);
+          if (!kGated && t.jv > 128) {
+            words(2, j_row + 128, a.j.tiled);
+            store_scales(sf + Stage::kISf + 4 * kGScaleTile, lane, r.w[2]);
+          }
         }
-        cur = nxt;
-        if (kTma) {
-          publish(n);
-        } else if (n >= kGLoadLag) {
-          cp_async_wait<kGLoadLag>();
-          publish(n - kGLoadLag);
+        if (!kTma) cp_async_wait<0>();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.full[s]);
+        skip(4);
+        ring.s += 4;
+        if (ring.s >= kStages) {
+          ring.s -= kStages;
+          ring.phase ^= 1;
         }
+        if (at.more) read();
       }
       cp_async_wait<0>();
-      if (!ok)
-        sm.gave_up = 1;
-      else if (!kTma)
-        for (uint32_t k = n > kGLoadLag ? n - kGLoadLag : 0; k < n; k++) publish(k);
+      if (!ok) sm.gave_up = 1;
     } else if (warp >= kGEpiWarp) {
       const int q = warp & 3;                       // accumulator lanes 32q .. 32q+31
       const int half = (warp - kGEpiWarp) >> 2;     // chunks of parity `half`
