@@ -16,6 +16,7 @@ at byte offsets K*o_g/2 and K*o_g/16).
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import Dict, Optional, Sequence
@@ -379,41 +380,58 @@ def col_matrix(out: Dict[str, torch.Tensor], scale_layout: int = NVFP4_SCALE_COM
     return matrix(out["col_data"], out["col_scale"], out["col_s2"], scale_layout)
 
 
-def _matrix(m: Dict[str, object], rows: int, elements: int, name: str) -> Matrix:
-    """``m`` checked to be ``rows`` factors and ``elements`` codes."""
-    for key, n in (("data", elements // 2), ("scale", elements // 16), ("s2", rows)):
-        if m[key].numel() != n:
-            raise ValueError(f"{name}[{key!r}] must have {n} entries, got {m[key].numel()}")
-    o = Matrix()
-    o.data = _dev(m["data"], torch.uint8, f"{name}['data']").value
-    o.scale = _dev(m["scale"], torch.uint8, f"{name}['scale']").value
-    o.s2 = _dev(m["s2"], torch.float32, f"{name}['s2']").value
-    o.scale_layout = int(m.get("scale_layout", NVFP4_SCALE_COMPACT))
-    return o
+def _ptr(t: Optional[torch.Tensor], dtype: torch.dtype, dev: torch.device, name: str) -> Optional[int]:
+    """Device address of a contiguous tensor of ``dtype`` on ``dev``."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _same_device(ref: torch.Tensor, *tensors) -> torch.device:
-    """The one CUDA device of all the tensors (None is skipped)."""
-    for t in tensors:
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"tensors are on {ref.device} and {t.device}")
-    if not ref.is_cuda:
-        raise ValueError("tensors must be CUDA tensors")
-    return ref.device
+def _cuda(t: torch.Tensor, name: str) -> torch.device:
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
 
 
-def _parts(*ms):
-    return [m[k] for m in ms for k in ("data", "scale", "s2")]
+def _matrix(m: Dict[str, object], rows: int, elements: int, dev: torch.device, name: str) -> Matrix:
+    """``m`` checked to be ``rows`` factors and ``elements`` codes on ``dev``."""
+    data, scale, s2 = m["data"], m["scale"], m["s2"]
+    if data.numel() * 2 != elements or scale.numel() * 16 != elements or s2.numel() != rows:
+        raise ValueError(f"{name} must hold {elements // 2} bytes of codes, {elements // 16} scales and {rows} factors, got "
+                         f"{data.numel()}, {scale.numel()} and {s2.numel()}")
+    return Matrix(_ptr(data, torch.uint8, dev, name), _ptr(scale, torch.uint8, dev, name),
+                  _ptr(s2, torch.float32, dev, name), m.get("scale_layout", NVFP4_SCALE_COMPACT))
 
 
-def _on(dev: torch.device, stream, what: str, call) -> None:
-    """Run ``call(stream pointer)`` with ``dev`` current, on its current stream
-    unless one is given."""
-    if stream is not None and stream.device != dev:
+def _split_array(m_splits: Sequence[int]):
+    """Host array of group sizes (kept alive by the caller during the call)."""
+    arr = array.array("q", m_splits)
+    return arr, arr.buffer_info()[0], len(arr)
+
+
+def _run(dev: torch.device, stream: Optional[torch.cuda.Stream], what: str, entry, *args) -> None:
+    """``entry(*args, stream)`` with ``dev`` current, on its current stream unless
+    one is given."""
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    with torch.cuda.device(dev):
-        rc = call(_stream(stream))
-    _check(rc, what)
+    else:
+        s = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev.index:
+        rc = entry(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = entry(*args, s)
+    if rc != NVFP4_OK:
+        raise NVFP4Error(what, rc)
 
 
 def _out_dtype(t: torch.Tensor, name: str) -> int:
@@ -424,13 +442,31 @@ def _out_dtype(t: torch.Tensor, name: str) -> int:
     raise ValueError(f"{name} must be float32 or bfloat16")
 
 
-def _width(w: Dict[str, object], x: Dict[str, object], rows: int, what: str) -> int:
+def _width(w: Dict[str, object], x: Dict[str, object], rows: int) -> int:
     """Contraction width of x [rows, K] against stacked weights w."""
-    ref, n = (x, rows) if rows else (w, w["s2"].numel())
-    total = 2 * ref["data"].numel()
+    m, n = (x, rows) if rows else (w, w["s2"].numel())
+    total = 2 * m["data"].numel()
     if n and total % n:
-        raise ValueError(f"{what}: {total} codes are not {n} equal rows")
+        raise ValueError(f"{total} codes are not {n} equal rows")
     return total // n if n else 0
+
+
+def _routing(first_dims: Optional[torch.Tensor], tensor_offsets: Optional[torch.Tensor], status: torch.Tensor, E: int,
+             dev: torch.device):
+    if tensor_offsets is not None and tensor_offsets.numel() != E + 1:
+        raise ValueError(f"tensor_offsets must have {E + 1} entries")
+    if status.numel() < 1:
+        raise ValueError("status must have an entry")
+    return (_ptr(first_dims, torch.int64, dev, "first_dims"), _ptr(tensor_offsets, torch.int64, dev, "tensor_offsets"),
+            _ptr(status, torch.int32, dev, "status"))
+
+
+def _gemm_args(x, w, y: torch.Tensor, E: int):
+    dev = _cuda(y, "y")
+    rows, N = y.shape
+    K = _width(w, x, rows)
+    return (dev, rows, N, K, _matrix(x, rows, rows * K, dev, "x"), _matrix(w, E * N, E * N * K, dev, "w"),
+            _ptr(y, y.dtype, dev, "y"), _out_dtype(y, "y"))
 
 
 def nvfp4_group_gemm(x: Dict[str, object], m_splits: Sequence[int], w: Dict[str, object], y: torch.Tensor,
@@ -438,45 +474,29 @@ def nvfp4_group_gemm(x: Dict[str, object], m_splits: Sequence[int], w: Dict[str,
     """y [rows, N] (bf16 or fp32) = X_g W_g^T for each group's rows of x [rows, K]
     and its matrix of w [E*N, K]. Input gradients: x the rowwise cast of dy, w
     the colwise cast of the weights."""
-    arr, E = _splits(m_splits)
-    rows, N = y.shape
-    K = _width(w, x, rows, "nvfp4_group_gemm")
-    dt = _out_dtype(y, "y")
-    dev = _same_device(y, *_parts(x, w))
-    xm, wm = _matrix(x, rows, rows * K, "x"), _matrix(w, E * N, E * N * K, "w")
-    yp = _dev(y, y.dtype, "y")
-    _on(dev, stream, "nvfp4_group_gemm", lambda s: lib().nvfp4_group_gemm(
-        ctypes.byref(xm), rows, K, arr, E, ctypes.byref(wm), N, yp, dt, s))
+    arr, ap, E = _split_array(m_splits)
+    dev, rows, N, K, xm, wm, yp, dt = _gemm_args(x, w, y, E)
+    _run(dev, stream, "nvfp4_group_gemm", lib().nvfp4_group_gemm, xm, rows, K, ap, E, wm, N, yp, dt)
 
 
 def nvfp4_group_gemm_graphsafe(x: Dict[str, object], first_dims: Optional[torch.Tensor],
                                tensor_offsets: Optional[torch.Tensor], w: Dict[str, object], y: torch.Tensor,
                                status: torch.Tensor, stream=None, num_groups: Optional[int] = None) -> None:
     E = _groups(first_dims, num_groups)
-    rows, N = y.shape
-    K = _width(w, x, rows, "nvfp4_group_gemm_graphsafe")
-    dt = _out_dtype(y, "y")
-    dev = _same_device(y, first_dims, tensor_offsets, status, *_parts(x, w))
-    xm, wm = _matrix(x, rows, rows * K, "x"), _matrix(w, E * N, E * N * K, "w")
-    fd, to, st, yp = _routing(first_dims, tensor_offsets, status, E) + (_dev(y, y.dtype, "y"),)
-    _on(dev, stream, "nvfp4_group_gemm_graphsafe", lambda s: lib().nvfp4_group_gemm_graphsafe(
-        ctypes.byref(xm), rows, K, fd, to, E, ctypes.byref(wm), N, yp, dt, st, s))
+    dev, rows, N, K, xm, wm, yp, dt = _gemm_args(x, w, y, E)
+    fd, to, st = _routing(first_dims, tensor_offsets, status, E, dev)
+    _run(dev, stream, "nvfp4_group_gemm_graphsafe", lib().nvfp4_group_gemm_graphsafe, xm, rows, K, fd, to, E, wm, N, yp, dt,
+         st)
 
 
-def _routing(first_dims, tensor_offsets, status, E: int):
-    if tensor_offsets is not None and tensor_offsets.numel() != E + 1:
-        raise ValueError(f"tensor_offsets must have {E + 1} entries")
-    return (_dev(first_dims, torch.int64, "first_dims"), _dev(tensor_offsets, torch.int64, "tensor_offsets"),
-            _dev(status, torch.int32, "status"))
-
-
-def _gated(x, w, h, gate_up, E):
+def _gated_args(x, w, h: torch.Tensor, gate_up: Optional[torch.Tensor], E: int):
+    dev = _cuda(h, "h")
     rows, F = h.shape
     if gate_up is not None and tuple(gate_up.shape) != (rows, 2 * F):
         raise ValueError("gate_up must be [rows, 2F]")
-    K = _width(w, x, rows, "nvfp4_group_gated_gemm")
-    return (rows, F, K, _matrix(x, rows, rows * K, "x"), _matrix(w, E * 2 * F, E * 2 * F * K, "w"),
-            _dev(h, torch.bfloat16, "h"), _dev(gate_up, torch.bfloat16, "gate_up"))
+    K = _width(w, x, rows)
+    return (dev, rows, F, K, _matrix(x, rows, rows * K, dev, "x"), _matrix(w, E * 2 * F, E * 2 * F * K, dev, "w"),
+            _ptr(h, torch.bfloat16, dev, "h"), _ptr(gate_up, torch.bfloat16, dev, "gate_up"))
 
 
 def nvfp4_group_gated_gemm(x: Dict[str, object], m_splits: Sequence[int], w: Dict[str, object], h: torch.Tensor,
@@ -484,11 +504,9 @@ def nvfp4_group_gated_gemm(x: Dict[str, object], m_splits: Sequence[int], w: Dic
     """h [rows, F] = silu(X_g Wgate_g^T) * (X_g Wup_g^T); w [E*2F, K] holds each
     group's gate rows, then its up rows. gate_up [rows, 2F], if given, takes the
     two projections (bf16) for the gradient."""
-    arr, E = _splits(m_splits)
-    dev = _same_device(h, gate_up, *_parts(x, w))
-    rows, F, K, xm, wm, hp, gp = _gated(x, w, h, gate_up, E)
-    _on(dev, stream, "nvfp4_group_gated_gemm", lambda s: lib().nvfp4_group_gated_gemm(
-        ctypes.byref(xm), rows, K, arr, E, ctypes.byref(wm), F, hp, gp, s))
+    arr, ap, E = _split_array(m_splits)
+    dev, rows, F, K, xm, wm, hp, gp = _gated_args(x, w, h, gate_up, E)
+    _run(dev, stream, "nvfp4_group_gated_gemm", lib().nvfp4_group_gated_gemm, xm, rows, K, ap, E, wm, F, hp, gp)
 
 
 def nvfp4_group_gated_gemm_graphsafe(x: Dict[str, object], first_dims: Optional[torch.Tensor],
@@ -496,49 +514,44 @@ def nvfp4_group_gated_gemm_graphsafe(x: Dict[str, object], first_dims: Optional[
                                      status: torch.Tensor, gate_up: Optional[torch.Tensor] = None, stream=None,
                                      num_groups: Optional[int] = None) -> None:
     E = _groups(first_dims, num_groups)
-    dev = _same_device(h, gate_up, first_dims, tensor_offsets, status, *_parts(x, w))
-    rows, F, K, xm, wm, hp, gp = _gated(x, w, h, gate_up, E)
-    fd, to, st = _routing(first_dims, tensor_offsets, status, E)
-    _on(dev, stream, "nvfp4_group_gated_gemm_graphsafe", lambda s: lib().nvfp4_group_gated_gemm_graphsafe(
-        ctypes.byref(xm), rows, K, fd, to, E, ctypes.byref(wm), F, hp, gp, st, s))
+    dev, rows, F, K, xm, wm, hp, gp = _gated_args(x, w, h, gate_up, E)
+    fd, to, st = _routing(first_dims, tensor_offsets, status, E, dev)
+    _run(dev, stream, "nvfp4_group_gated_gemm_graphsafe", lib().nvfp4_group_gated_gemm_graphsafe, xm, rows, K, fd, to, E, wm,
+         F, hp, gp, st)
 
 
-def _wgrad(dy, x, dw, rows):
+def _wgrad_args(dy, x, dw: torch.Tensor, rows: int, groups: int):
+    dev = _cuda(dw, "dw")
     E, N, K = dw.shape
-    return (E, N, K, _matrix(dy, E * N, rows * N, "dy"), _matrix(x, E * K, rows * K, "x"),
-            _dev(dw, dw.dtype, "dw"), _out_dtype(dw, "dw"))
+    if E != groups:
+        raise ValueError(f"dw must have {groups} matrices")
+    return (dev, E, N, K, _matrix(dy, E * N, rows * N, dev, "dy"), _matrix(x, E * K, rows * K, dev, "x"),
+            _ptr(dw, dw.dtype, dev, "dw"), _out_dtype(dw, "dw"))
 
 
 def nvfp4_group_wgrad(dy: Dict[str, object], x: Dict[str, object], m_splits: Sequence[int], dw: torch.Tensor,
                       stream=None) -> None:
     """dw [E, N, K] (bf16 or fp32) = dY_g^T X_g from the colwise casts of dy
     [rows, N] and x [rows, K]; zero for an empty group."""
-    arr, E = _splits(m_splits)
-    if dw.shape[0] != E:
-        raise ValueError(f"dw must have {E} matrices")
-    rows = sum(int(m) for m in m_splits)
-    dev = _same_device(dw, *_parts(dy, x))
-    E, N, K, dm, xm, wp, dt = _wgrad(dy, x, dw, rows)
-    _on(dev, stream, "nvfp4_group_wgrad", lambda s: lib().nvfp4_group_wgrad(
-        ctypes.byref(dm), ctypes.byref(xm), rows, arr, E, N, K, wp, dt, s))
+    arr, ap, groups = _split_array(m_splits)
+    rows = sum(arr)
+    dev, E, N, K, dm, xm, wp, dt = _wgrad_args(dy, x, dw, rows, groups)
+    _run(dev, stream, "nvfp4_group_wgrad", lib().nvfp4_group_wgrad, dm, xm, rows, ap, E, N, K, wp, dt)
 
 
 def nvfp4_group_wgrad_graphsafe(dy: Dict[str, object], x: Dict[str, object], capacity_rows: int,
                                 first_dims: Optional[torch.Tensor], tensor_offsets: Optional[torch.Tensor],
                                 dw: torch.Tensor, status: torch.Tensor, stream=None,
                                 num_groups: Optional[int] = None) -> None:
-    E = _groups(first_dims, num_groups)
-    if dw.shape[0] != E:
-        raise ValueError(f"dw must have {E} matrices")
     rows = int(capacity_rows)
-    dev = _same_device(dw, first_dims, tensor_offsets, status, *_parts(dy, x))
-    E, N, K, dm, xm, wp, dt = _wgrad(dy, x, dw, rows)
-    fd, to, st = _routing(first_dims, tensor_offsets, status, E)
-    _on(dev, stream, "nvfp4_group_wgrad_graphsafe", lambda s: lib().nvfp4_group_wgrad_graphsafe(
-        ctypes.byref(dm), ctypes.byref(xm), rows, fd, to, E, N, K, wp, dt, st, s))
+    dev, E, N, K, dm, xm, wp, dt = _wgrad_args(dy, x, dw, rows, _groups(first_dims, num_groups))
+    fd, to, st = _routing(first_dims, tensor_offsets, status, E, dev)
+    _run(dev, stream, "nvfp4_group_wgrad_graphsafe", lib().nvfp4_group_wgrad_graphsafe, dm, xm, rows, fd, to, E, N, K, wp, dt,
+         st)
 
 
-def _gated_backward(dh, gate_up, d_gate_up, row_amax, col_amax, E):
+def _gated_backward_args(dh, gate_up, d_gate_up, row_amax, col_amax, E: int):
+    dev = _cuda(dh, "dh")
     rows, F = dh.shape
     for t, name in ((gate_up, "gate_up"), (d_gate_up, "d_gate_up")):
         if tuple(t.shape) != (rows, 2 * F):
@@ -546,9 +559,9 @@ def _gated_backward(dh, gate_up, d_gate_up, row_amax, col_amax, E):
     for t, n, name in ((row_amax, rows, "row_amax"), (col_amax, E * 2 * F, "col_amax")):
         if t is not None and t.numel() != n:
             raise ValueError(f"{name} must have {n} entries")
-    return (rows, F, _dev(dh, torch.bfloat16, "dh"), _dev(gate_up, torch.bfloat16, "gate_up"),
-            _dev(d_gate_up, torch.bfloat16, "d_gate_up"), _dev(row_amax, torch.float32, "row_amax"),
-            _dev(col_amax, torch.float32, "col_amax"))
+    return (dev, rows, F, _ptr(dh, torch.bfloat16, dev, "dh"), _ptr(gate_up, torch.bfloat16, dev, "gate_up"),
+            _ptr(d_gate_up, torch.bfloat16, dev, "d_gate_up"), _ptr(row_amax, torch.float32, dev, "row_amax"),
+            _ptr(col_amax, torch.float32, dev, "col_amax"))
 
 
 def nvfp4_group_gated_backward(dh: torch.Tensor, gate_up: torch.Tensor, m_splits: Sequence[int],
@@ -557,11 +570,9 @@ def nvfp4_group_gated_backward(dh: torch.Tensor, gate_up: torch.Tensor, m_splits
     """d_gate_up [rows, 2F] from dh [rows, F] and the saved gate_up [rows, 2F]
     of nvfp4_group_gated_gemm, with the row amax [rows] and per-group column
     amax [E*2F] its cast takes. d_gate_up may be gate_up."""
-    arr, E = _splits(m_splits)
-    dev = _same_device(dh, gate_up, d_gate_up, row_amax, col_amax)
-    rows, F, dp, gp, op, rp, cp = _gated_backward(dh, gate_up, d_gate_up, row_amax, col_amax, E)
-    _on(dev, stream, "nvfp4_group_gated_backward", lambda s: lib().nvfp4_group_gated_backward(
-        dp, gp, rows, F, arr, E, op, rp, cp, s))
+    arr, ap, E = _split_array(m_splits)
+    dev, rows, F, dp, gp, op, rp, cp = _gated_backward_args(dh, gate_up, d_gate_up, row_amax, col_amax, E)
+    _run(dev, stream, "nvfp4_group_gated_backward", lib().nvfp4_group_gated_backward, dp, gp, rows, F, ap, E, op, rp, cp)
 
 
 def nvfp4_group_gated_backward_graphsafe(dh: torch.Tensor, gate_up: torch.Tensor, first_dims: Optional[torch.Tensor],
@@ -570,11 +581,10 @@ def nvfp4_group_gated_backward_graphsafe(dh: torch.Tensor, gate_up: torch.Tensor
                                          col_amax: Optional[torch.Tensor] = None, stream=None,
                                          num_groups: Optional[int] = None) -> None:
     E = _groups(first_dims, num_groups)
-    dev = _same_device(dh, gate_up, d_gate_up, row_amax, col_amax, first_dims, tensor_offsets, status)
-    rows, F, dp, gp, op, rp, cp = _gated_backward(dh, gate_up, d_gate_up, row_amax, col_amax, E)
-    fd, to, st = _routing(first_dims, tensor_offsets, status, E)
-    _on(dev, stream, "nvfp4_group_gated_backward_graphsafe", lambda s: lib().nvfp4_group_gated_backward_graphsafe(
-        dp, gp, rows, F, fd, to, E, op, rp, cp, st, s))
+    dev, rows, F, dp, gp, op, rp, cp = _gated_backward_args(dh, gate_up, d_gate_up, row_amax, col_amax, E)
+    fd, to, st = _routing(first_dims, tensor_offsets, status, E, dev)
+    _run(dev, stream, "nvfp4_group_gated_backward_graphsafe", lib().nvfp4_group_gated_backward_graphsafe, dp, gp, rows, F, fd,
+         to, E, op, rp, cp, st)
 
 
 def nvfp4_adapter_workspace_bytes(rows: int, rank: int) -> int:
@@ -587,23 +597,20 @@ def nvfp4_adapter_gemm(x_bf16: torch.Tensor, x: Dict[str, object], w: Dict[str, 
     """y [rows, N] = X W^T + factor[i] (x A_i^T) B_i^T with i = ids[t] (-1: none).
     x_bf16 [rows, K] and its rowwise cast x, w [N, K], a [L, R, K], b [L, N, R],
     factor [L], ids int32 [rows]; workspace from alloc_adapter_workspace."""
+    dev = _cuda(y, "y")
     rows, K = x_bf16.shape
-    L, R = a.shape[0], a.shape[1]
-    N = y.shape[1]
-    if y.shape[0] != rows or ids.numel() != rows or factor.numel() != L:
+    N, (L, R) = y.shape[1], a.shape[:2]
+    if y.shape[0] != rows or ids.numel() != rows or factor.numel() != L or status.numel() < 1:
         raise ValueError("y and ids must have a row for each of x_bf16's, factor an entry for each adapter")
-    if tuple(a.shape) != (L, R, K) or tuple(b.shape) != (L, N, R):
+    if a.shape[2] != K or tuple(b.shape) != (L, N, R):
         raise ValueError("a must be [L, R, K] and b [L, N, R]")
-    dt = _out_dtype(y, "y")
-    dev = _same_device(y, x_bf16, a, b, factor, ids, workspace, status, *_parts(x, w))
-    xm, wm = _matrix(x, rows, rows * K, "x"), _matrix(w, N, N * K, "w")
-    wp, wb = _workspace(workspace)
-    ptrs = (_dev(x_bf16, torch.bfloat16, "x_bf16"), _dev(a, torch.bfloat16, "a"), _dev(b, torch.bfloat16, "b"),
-            _dev(factor, torch.float32, "factor"), _dev(ids, torch.int32, "ids"), _dev(y, y.dtype, "y"),
-            _dev(status, torch.int32, "status"))
-    xp, ap, bp, fp, ip, yp, st = ptrs
-    _on(dev, stream, "nvfp4_adapter_gemm", lambda s: lib().nvfp4_adapter_gemm(
-        xp, ctypes.byref(xm), rows, K, ctypes.byref(wm), N, ap, bp, fp, L, R, ip, yp, dt, wp, wb, st, s))
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    _run(dev, stream, "nvfp4_adapter_gemm", lib().nvfp4_adapter_gemm, _ptr(x_bf16, torch.bfloat16, dev, "x_bf16"),
+         _matrix(x, rows, rows * K, dev, "x"), rows, K, _matrix(w, N, N * K, dev, "w"), N,
+         _ptr(a, torch.bfloat16, dev, "a"), _ptr(b, torch.bfloat16, dev, "b"), _ptr(factor, torch.float32, dev, "factor"),
+         L, R, _ptr(ids, torch.int32, dev, "ids"), _ptr(y, y.dtype, dev, "y"), _out_dtype(y, "y"),
+         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(status, torch.int32, dev, "status"))
 
 
 def alloc_adapter_workspace(rows: int, rank: int, device="cuda") -> torch.Tensor:

@@ -516,32 +516,51 @@ __device__ __forceinline__ void add_adapters(uint64_t (&y2)[16], const GemmArgs&
   uint64_t acc[32];
 #pragma unroll
   for (int k = 0; k < 32; k++) acc[k] = (k & 1 ? y2[k >> 1] >> 32 : y2[k >> 1] & 0xFFFFFFFFu);
-  auto dot8 = [&](uint64_t& c, const uint4& w, const float* up) {
-    const float4 u0 = gload(reinterpret_cast<const float4*>(up)), u1 = gload(reinterpret_cast<const float4*>(up) + 1);
-    c = fma2x(pack2(u0.x, u0.y), unpack2(w.x), c);
-    c = fma2x(pack2(u0.z, u0.w), unpack2(w.y), c);
-    c = fma2x(pack2(u1.x, u1.y), unpack2(w.z), c);
-    c = fma2x(pack2(u1.z, u1.w), unpack2(w.w), c);
-  };
+  // No branches around the loads of single rows, so that many are in flight:
+  // rows behind the last read the last again, rows without an adapter nothing.
+  const float4* u4 = reinterpret_cast<const float4*>(u);
+  const int pitch4 = a.rank / 4;
+#pragma unroll 1
   for (int r = 0; r < a.rank; r += 8) {
     if (same) {
       const uint4 w = gload(reinterpret_cast<const uint4*>(b + id0 * pitch + r));
+      const uint64_t w2[4] = {unpack2(w.x), unpack2(w.y), unpack2(w.z), unpack2(w.w)};
 #pragma unroll
-      for (int k = 0; k < 32; k++)
-        if (k < nc) dot8(acc[k], w, u + k * a.rank + r);
+      for (int k = 0; k < 32; k++) {
+        const float4* up = u4 + min(k, nc - 1) * pitch4 + r / 4;
+        const float4 u0 = gload(up), u1 = gload(up + 1);
+        acc[k] = fma2x(pack2(u0.x, u0.y), w2[0], acc[k]);
+        acc[k] = fma2x(pack2(u0.z, u0.w), w2[1], acc[k]);
+        acc[k] = fma2x(pack2(u1.x, u1.y), w2[2], acc[k]);
+        acc[k] = fma2x(pack2(u1.z, u1.w), w2[3], acc[k]);
+      }
     } else {
 #pragma unroll
-      for (int k0 = 0; k0 < 32; k0 += 4) {
-        uint4 w[4];
-        int32_t ik[4];
+      for (int k0 = 0; k0 < 32; k0 += 8) {
+        if (k0 >= nc) break;
+        uint4 w[8];
+        bool in[8];
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
-          ik[k] = __shfl_sync(0xFFFFFFFFu, id, k0 + k);
-          if (ik[k] >= 0) w[k] = gload(reinterpret_cast<const uint4*>(b + ik[k] * pitch + r));
+        for (int k = 0; k < 8; k++) {
+          const int32_t ik = __shfl_sync(0xFFFFFFFFu, id, k0 + k);
+          in[k] = ik >= 0;
+          w[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (in[k]) w[k] = gload(reinterpret_cast<const uint4*>(b + ik * pitch + r));
         }
 #pragma unroll
-        for (int k = 0; k < 4; k++)
-          if (ik[k] >= 0) dot8(acc[k0 + k], w[k], u + (k0 + k) * a.rank + r);
+        for (int k = 0; k < 8; k++) {
+          const float4* up = u4 + (k0 + k) * pitch4 + r / 4;
+          float4 u0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u1 = u0;
+          if (in[k]) {
+            u0 = gload(up);
+            u1 = gload(up + 1);
+          }
+          uint64_t& c = acc[k0 + k];
+          c = fma2x(pack2(u0.x, u0.y), unpack2(w[k].x), c);
+          c = fma2x(pack2(u0.z, u0.w), unpack2(w[k].y), c);
+          c = fma2x(pack2(u1.x, u1.y), unpack2(w[k].z), c);
+          c = fma2x(pack2(u1.z, u1.w), unpack2(w[k].w), c);
+        }
       }
     }
   }
