@@ -35,7 +35,7 @@ constexpr int kAdMaxRank = 64;
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -63,23 +63,20 @@ adapter_shrink_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict
   const int rank = static_cast<int>(cluster.block_rank());
   const int slot = blockIdx.y;
   const int32_t t0 = static_cast<int32_t>(blockIdx.x / cn) * kTok;
-  if (t < kTok) {
-    int32_t a = t0 + t < rows ? gload(&ids[t0 + t]) : -1;
+  // the block's distinct adapters, in the order of their first tokens: one warp,
+  // a lane for each token
+  if (warp == 0) {
+    int32_t a = lane < kTok && t0 + lane < rows ? gload(&ids[t0 + lane]) : -1;
     if (a >= adapters || a < -1) {
       if (slot == 0 && rank == 0) gstore(status, static_cast<int32_t>(NVFP4_ERR_ROUTING));
       a = -1;
     }
-    id[t] = a;
-  }
-  __syncthreads();
-  if (t == 0) {
-    int n = 0;
-    for (int i = 0; i < kTok; i++) {
-      bool seen = id[i] < 0;
-      for (int j = 0; j < n; j++) seen = seen || distinct[j] == id[i];
-      if (!seen) distinct[n++] = id[i];
-    }
-    count = n;
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, a);
+    const bool first = a >= 0 && __ffs(same) - 1 == lane;
+    const uint32_t firsts = __ballot_sync(0xFFFFFFFFu, first);
+    if (lane < kTok) id[lane] = a;
+    if (first) distinct[__popc(firsts & ((1u << lane) - 1))] = a;
+    if (lane == 0) count = __popc(firsts);
   }
   __syncthreads();
   const int n = count;
@@ -89,7 +86,12 @@ adapter_shrink_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict
   const int s0 = static_cast<int>(static_cast<int64_t>(steps) * part / parts);
   const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (part + 1) / parts);
   const int gr = lane >> 2, kq = (lane & 3) * 8;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  // rows behind the last read the last one again: no branches around the loads
+  const uint16_t* xr[kMT][2];
+#pragma unroll
+  for (int m = 0; m < kMT; m++)
+#pragma unroll
+    for (int h = 0; h < 2; h++) xr[m][h] = x + static_cast<int64_t>(min(t0 + 16 * m + 8 * h + gr, rows - 1)) * K + kq;
   // the loop count is the same in every CTA of the cluster (same tokens, same slot)
   for (int d = slot; d < n; d += slots) {
     const int32_t a = distinct[d];
@@ -101,21 +103,17 @@ adapter_shrink_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict
       for (int c = 0; c < kNT; c++)
 #pragma unroll
         for (int e = 0; e < 4; e++) acc[m][c][e] = 0.0f;
-#pragma unroll 4
-    for (int s = s0; s < s1; s++) {
-      const int k = s * 32 + kq;
-      const bool in = k < K;
+    const uint16_t* ar = Aa + static_cast<int64_t>(gr) * K + kq;
+    auto step = [&](int k, bool in) {
       uint4 xv[kMT][2], bv[kNT];
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int m = 0; m < kMT; m++)
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-          const int64_t r = t0 + 16 * m + 8 * h + gr;
-          xv[m][h] = in && r < rows ? ld_u4(reinterpret_cast<const uint4*>(x + r * K + k)) : zero;
-        }
+        for (int h = 0; h < 2; h++) xv[m][h] = in ? ld_u4(reinterpret_cast<const uint4*>(xr[m][h] + k)) : zero;
 #pragma unroll
       for (int c = 0; c < kNT; c++)
-        bv[c] = in ? ld_u4(reinterpret_cast<const uint4*>(Aa + static_cast<int64_t>(8 * c + gr) * K + k)) : zero;
+        bv[c] = in ? ld_u4(reinterpret_cast<const uint4*>(ar + static_cast<int64_t>(8 * c) * K + k)) : zero;
 #pragma unroll
       for (int m = 0; m < kMT; m++)
 #pragma unroll
@@ -123,7 +121,11 @@ adapter_shrink_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict
           mma_bf16(acc[m][c], xv[m][0].x, xv[m][1].x, xv[m][0].y, xv[m][1].y, bv[c].x, bv[c].y);
           mma_bf16(acc[m][c], xv[m][0].z, xv[m][1].z, xv[m][0].w, xv[m][1].w, bv[c].z, bv[c].w);
         }
-    }
+    };
+    const int whole = min(s1, K / 32);
+#pragma unroll 4
+    for (int s = s0; s < whole; s++) step(32 * s, true);
+    if (s1 > whole && s1 > s0) step(32 * (s1 - 1), 32 * (s1 - 1) + kq < K);  // the last half step of a K off the 32s
     float* mine = partial + warp * kTok * kR;
 #pragma unroll
     for (int m = 0; m < kMT; m++)
