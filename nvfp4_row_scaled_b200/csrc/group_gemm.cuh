@@ -61,6 +61,7 @@
 #include <cuda.h>
 
 #include "group_cast.cuh"
+#include "adapter.cuh"
 #include "post_scale.cuh"
 #include "routing.cuh"
 
@@ -106,7 +107,7 @@ struct GemmArgs {
   int32_t ni;        // output columns: I rows of a group (gated: of each half)
   int32_t nj;        // wgrad: J rows of a group
   int32_t K;         // contraction (wgrad: the group's rows instead)
-  int32_t jt, jt_log;       // J rows of a tile: 32, 64, 128 or 256; its logarithm
+  int32_t jt, jt_log;       // J rows of a tile: a power of two, 16 to 256; its logarithm
   uint32_t it, it_magic;    // I tiles of a group; floor(2^32 / it), 2^32 - 1 for it = 1
   int32_t jbulk;     // nonzero: J scales by bulk copies (tiled, and J tiles of whole 128-row blocks)
   int32_t loaders;   // nonzero: warps 2-5 take part
@@ -497,75 +498,128 @@ __device__ __forceinline__ void store_bf16(const uint32_t (&y)[16], uint32_t (&t
   }
 }
 
-// The adapters' share of a lane's 32 outputs (feature n of rows row .. row + nc - 1):
-// y[k] += sum_r u[row + k][r] b[id][n][r] (y2: pairs of rows), in fp32, ranks in order in two
-// interleaved sums (even and odd). Rows of one adapter, the rule in a prompt,
-// read the lane's row of B once; other rows read theirs eight ranks at a time,
-// several rows in flight.
-__device__ __forceinline__ void add_adapters(uint64_t (&y2)[16], const GemmArgs& a, int64_t row, int64_t n, int nc, int lane,
-                                             bool live) {
+// Three bf16 pairs whose sum is two fp32 values to 2^-25 of each: rounded, the
+// rest rounded, the rest of that.
+__device__ __forceinline__ void split3(float a, float b, uint32_t (&p)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; i++) {
+    p[i] = bf16x2_rn(a, b);
+    a -= __uint_as_float(p[i] << 16);
+    b -= __uint_as_float(p[i] & 0xFFFF0000u);
+  }
+}
+
+// The adapters' share of a warp's 32 features x 32 rows (lane = feature n0 + lane,
+// y2[i] = rows 2i and 2i + 1 of row .. row + nc - 1):
+//   y += sum_r u[row][r] b[id][n][r]
+// on the bf16 tensor cores, 16 features x 8 rows x 16 ranks an instruction. u is
+// fp32 and stays so: three bf16 terms of it multiply b and meet in the fp32
+// accumulator. Each distinct adapter of the rows is one pass over the 8-row
+// blocks that use it, with the other rows' u as zeros -- which add nothing, so a
+// row's result does not depend on its neighbours; the next pass's b is loaded
+// meanwhile. The ranks are numbered as a lane loads them (8 of a row, 16 bytes),
+// alike on both sides. The sums then change from the instruction's layout to
+// lane = feature in shared memory. (In fp32 FMAs, 8 ranks x 32 rows a step, this
+// took 60 k cycles of a 128 x 256 tile's epilogue at rank 32.)
+__device__ __forceinline__ void add_adapters(uint64_t (&y2)[16], uint32_t (&turn)[16][32], const GemmArgs& a,
+                                             int64_t row, int64_t n0, int features, int nc, int lane) {
   int32_t id = lane < nc ? gload(&a.ids[row + lane]) : -1;
   if (id < 0 || id >= a.adapters) id = -1;
-  if (!__any_sync(0xFFFFFFFFu, id >= 0)) return;
-  const int32_t id0 = __shfl_sync(0xFFFFFFFFu, id, 0);
-  const bool same = __all_sync(0xFFFFFFFFu, lane >= nc || id == id0);
-  const int64_t nn = live ? n : 0;  // a lane past the features computes on feature 0 and stores nothing
-  const float* u = a.u + row * a.rank;
-  const uint16_t* b = a.b + nn * a.rank;
+  const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);
+  uint32_t firsts = __ballot_sync(0xFFFFFFFFu, id >= 0 && __ffs(same) - 1 == lane);
+  if (firsts == 0) return;
+  const int gr = lane >> 2, q8 = (lane & 3) * 8;
   const int64_t pitch = static_cast<int64_t>(a.ni) * a.rank;
-  uint64_t acc[32];
+  const uint16_t* b = a.b + (n0 + gr) * a.rank + q8;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  uint4 w[2][2], wn[2][2];  // features 16 m + 8 h + gr, ranks r + q8 .. + 7
+  auto load_b = [&](int32_t i, int r, uint4(&v)[2][2]) {
 #pragma unroll
-  for (int k = 0; k < 32; k++) acc[k] = (k & 1 ? y2[k >> 1] >> 32 : y2[k >> 1] & 0xFFFFFFFFu);
-  // No branches around the loads of single rows, so that many are in flight:
-  // rows behind the last read the last again, rows without an adapter nothing.
-  const float4* u4 = reinterpret_cast<const float4*>(u);
-  const int pitch4 = a.rank / 4;
+    for (int m = 0; m < 2; m++)
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+        v[m][h] = r + q8 < a.rank && 16 * m + 8 * h + gr < features
+                      ? gload(reinterpret_cast<const uint4*>(b + i * pitch + (16 * m + 8 * h) * a.rank + r))
+                      : zero;
+  };
+  float acc[2][4][4];
+#pragma unroll
+  for (int m = 0; m < 2; m++)
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) acc[m][j][e] = 0.0f;
+  int first = __ffs(firsts) - 1;
+  firsts &= firsts - 1;
+  int32_t cur = __shfl_sync(0xFFFFFFFFu, id, first);
+  int r = 0;
+  load_b(cur, 0, w);
 #pragma unroll 1
-  for (int r = 0; r < a.rank; r += 8) {
-    if (same) {
-      const uint4 w = gload(reinterpret_cast<const uint4*>(b + id0 * pitch + r));
-      const uint64_t w2[4] = {unpack2(w.x), unpack2(w.y), unpack2(w.z), unpack2(w.w)};
-#pragma unroll
-      for (int k = 0; k < 32; k++) {
-        const float4* up = u4 + min(k, nc - 1) * pitch4 + r / 4;
-        const float4 u0 = gload(up), u1 = gload(up + 1);
-        acc[k] = fma2x(pack2(u0.x, u0.y), w2[0], acc[k]);
-        acc[k] = fma2x(pack2(u0.z, u0.w), w2[1], acc[k]);
-        acc[k] = fma2x(pack2(u1.x, u1.y), w2[2], acc[k]);
-        acc[k] = fma2x(pack2(u1.z, u1.w), w2[3], acc[k]);
-      }
-    } else {
-#pragma unroll
-      for (int k0 = 0; k0 < 32; k0 += 8) {
-        if (k0 >= nc) break;
-        uint4 w[8];
-        bool in[8];
-#pragma unroll
-        for (int k = 0; k < 8; k++) {
-          const int32_t ik = __shfl_sync(0xFFFFFFFFu, id, k0 + k);
-          in[k] = ik >= 0;
-          w[k] = make_uint4(0u, 0u, 0u, 0u);
-          if (in[k]) w[k] = gload(reinterpret_cast<const uint4*>(b + ik * pitch + r));
-        }
-#pragma unroll
-        for (int k = 0; k < 8; k++) {
-          const float4* up = u4 + (k0 + k) * pitch4 + r / 4;
-          float4 u0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u1 = u0;
-          if (in[k]) {
-            u0 = gload(up);
-            u1 = gload(up + 1);
-          }
-          uint64_t& c = acc[k0 + k];
-          c = fma2x(pack2(u0.x, u0.y), unpack2(w[k].x), c);
-          c = fma2x(pack2(u0.z, u0.w), unpack2(w[k].y), c);
-          c = fma2x(pack2(u1.x, u1.y), unpack2(w[k].z), c);
-          c = fma2x(pack2(u1.z, u1.w), unpack2(w[k].w), c);
-        }
+  while (true) {
+    // the step after this one: the next 32 ranks, or the next adapter
+    int32_t nxt = cur;
+    int rn = r + 32;
+    bool more = true;
+    if (rn >= a.rank) {
+      rn = 0;
+      more = firsts != 0;
+      if (more) {
+        nxt = __shfl_sync(0xFFFFFFFFu, id, __ffs(firsts) - 1);
+        firsts &= firsts - 1;
       }
     }
-  }
+    if (more) load_b(nxt, rn, wn);
+    const uint32_t users = __ballot_sync(0xFFFFFFFFu, id == cur);
 #pragma unroll
-  for (int k = 0; k < 16; k++) y2[k] = pack2(lo2(acc[2 * k]) + hi2(acc[2 * k]), lo2(acc[2 * k + 1]) + hi2(acc[2 * k + 1]));
+    for (int j = 0; j < 4; j++) {
+      if (((users >> (8 * j)) & 0xFF) == 0) continue;
+      float4 u0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u1 = u0;
+      if (((users >> (8 * j + gr)) & 1) && r + q8 < a.rank) {
+        const float4* up = reinterpret_cast<const float4*>(a.u + (row + 8 * j + gr) * a.rank + r + q8);
+        u0 = gload(up);
+        u1 = gload(up + 1);
+      }
+      uint32_t p[4][3];
+      split3(u0.x, u0.y, p[0]);
+      split3(u0.z, u0.w, p[1]);
+      split3(u1.x, u1.y, p[2]);
+      split3(u1.z, u1.w, p[3]);
+#pragma unroll
+      for (int i = 2; i >= 0; i--)
+#pragma unroll
+        for (int m = 0; m < 2; m++) {
+          mma_bf16(acc[m][j], w[m][0].x, w[m][1].x, w[m][0].y, w[m][1].y, p[0][i], p[1][i]);
+          mma_bf16(acc[m][j], w[m][0].z, w[m][1].z, w[m][0].w, w[m][1].w, p[2][i], p[3][i]);
+        }
+    }
+    if (!more) break;
+    cur = nxt;
+    r = rn;
+#pragma unroll
+    for (int m = 0; m < 2; m++)
+#pragma unroll
+      for (int h = 0; h < 2; h++) w[m][h] = wn[m][h];
+  }
+  // 16 rows at a time: [row][feature], the features' blocks of 8 exchanged by row
+  // pair so that the four row pairs of an instruction lie in different banks
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    __syncwarp();
+#pragma unroll
+    for (int m = 0; m < 2; m++)
+#pragma unroll
+      for (int j = 0; j < 2; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+          turn[8 * j + (q8 >> 2) + (e & 1)][(16 * m + 8 * (e >> 1) + gr) ^ q8] = __float_as_uint(acc[m][2 * h + j][e]);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      const int f = lane ^ ((k & 3) << 3);
+      uint64_t& y = y2[8 * h + k];
+      y = pack2(lo2(y) + __uint_as_float(turn[2 * k][f]), hi2(y) + __uint_as_float(turn[2 * k + 1][f]));
+    }
+  }
 }
 
 // One stage's scale copies and MMAs, by one thread. All descriptors are one
@@ -1024,7 +1078,7 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
             for (int k = 0; k < 16; k++) b[k] = bf16x2_rn(silu(lo2(y[k])) * lo2(z[k]), silu(hi2(y[k])) * hi2(z[k]));
             store_bf16(b, turn, static_cast<uint16_t*>(a.out) + row * a.ni + t.i0 + 32 * q, a.ni, nc, features, lane);
           } else {
-            if (kMode == kGemmAdapter) add_adapters(y, a, row, n, nc, lane, live);
+            if (kMode == kGemmAdapter) add_adapters(y, turn, a, row, t.i0 + 32 * q, features, nc, lane);
             if (a.out_f32) {
               float* o = static_cast<float*>(a.out) + row * a.ni + n;
 #pragma unroll

@@ -29,7 +29,6 @@
 #include "mx_cast.cuh"
 #include "group_gemm.cuh"
 #include "gated_backward.cuh"
-#include "adapter.cuh"
 
 using namespace nvfp4rs;
 
@@ -699,7 +698,7 @@ nvfp4_status launch_gemm(const Routing& routing, GemmArgs a, int64_t rows, int64
     do {
       a.jt /= 2;
       tiles = product_tiles(routing, rows, a.nj, it1, a.jt, kWgrad);
-    } while (a.jt > 32 && tiles < sms);
+    } while (a.jt > (kMode == kGemmAdapter ? 16 : 32) && tiles < sms);
   }
   if (tiles == 0) return NVFP4_OK;
   if (tiles > INT32_MAX) return NVFP4_ERR_UNSUPPORTED;
