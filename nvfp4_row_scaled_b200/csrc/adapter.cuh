@@ -48,7 +48,7 @@ __device__ __forceinline__ uint4 ld_u4(const uint4* p) {
 
 // kNT = rank / 8 column tiles. partial: dynamic shared [8 warps][16 kMT][8 kNT] floats.
 template <int kMT, int kNT>
-__global__ void __launch_bounds__(kAdThreads)
+__global__ void __launch_bounds__(kAdThreads, 2)
 adapter_shrink_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ A, const float* __restrict__ factor,
                       const int32_t* __restrict__ ids, float* __restrict__ u, int32_t* __restrict__ status,
                       int32_t rows, int32_t K, int32_t adapters, int32_t cn, int32_t slots) {

@@ -509,99 +509,104 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t (&p)[3]) {
   }
 }
 
-// The adapters' share of a warp's 32 features x 32 rows (lane = feature n0 + lane,
-// y2[i] = rows 2i and 2i + 1 of row .. row + nc - 1):
-//   y += sum_r u[row][r] b[id][n][r]
-// on the bf16 tensor cores, 16 features x 8 rows x 16 ranks an instruction. u is
-// fp32 and stays so: three bf16 terms of it multiply b and meet in the fp32
-// accumulator. Each distinct adapter of the rows is one pass over the 8-row
-// blocks that use it, with the other rows' u as zeros -- which add nothing, so a
-// row's result does not depend on its neighbours; the next pass's b is loaded
-// meanwhile. The ranks are numbered as a lane loads them (8 of a row, 16 bytes),
-// alike on both sides. The sums then change from the instruction's layout to
-// lane = feature in shared memory. (In fp32 FMAs, 8 ranks x 32 rows a step, this
-// took 60 k cycles of a 128 x 256 tile's epilogue at rank 32.)
-__device__ __forceinline__ void add_adapters(uint64_t (&y2)[16], uint32_t (&turn)[16][32], const GemmArgs& a,
-                                             int64_t row, int64_t n0, int features, int nc, int lane) {
-  int32_t id = lane < nc ? gload(&a.ids[row + lane]) : -1;
-  if (id < 0 || id >= a.adapters) id = -1;
-  const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);
-  uint32_t firsts = __ballot_sync(0xFFFFFFFFu, id >= 0 && __ffs(same) - 1 == lane);
-  if (firsts == 0) return;
-  const int gr = lane >> 2, q8 = (lane & 3) * 8;
-  const int64_t pitch = static_cast<int64_t>(a.ni) * a.rank;
-  const uint16_t* b = a.b + (n0 + gr) * a.rank + q8;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  uint4 w[2][2], wn[2][2];  // features 16 m + 8 h + gr, ranks r + q8 .. + 7
-  auto load_b = [&](int32_t i, int r, uint4(&v)[2][2]) {
-#pragma unroll
-    for (int m = 0; m < 2; m++)
-#pragma unroll
-      for (int h = 0; h < 2; h++)
-        v[m][h] = r + q8 < a.rank && 16 * m + 8 * h + gr < features
-                      ? gload(reinterpret_cast<const uint4*>(b + i * pitch + (16 * m + 8 * h) * a.rank + r))
-                      : zero;
-  };
-  float acc[2][4][4];
+// The adapters' share of a warp's 32 features x 32 rows (features n0 .., rows
+// row .. row + nc - 1): sum_r u[row][r] b[id][n][r], on the bf16 tensor cores, 16
+// features x 8 rows x 16 ranks an instruction. u is fp32 and stays so: three bf16
+// terms of it multiply b and meet in the fp32 accumulator. Each distinct adapter
+// of the rows is one pass over the 8-row blocks that use it, with the other
+// rows' u as zeros -- which add nothing, so a row's result does not depend on
+// its neighbours; the next pass's b is loaded meanwhile. The ranks are numbered as a
+// lane loads them (8 of a row, 16 bytes), alike on both sides. Reads nothing of
+// the projection, so a tile's first chunk is summed while the tile is still being
+// multiplied. (In fp32 FMAs, 8 ranks x 32 rows a step, this took 60 k cycles of
+// a 128 x 256 tile's epilogue at rank 32.)
+// acc[m][j][e]: feature 16 m + 8 (e / 2) + lane / 4, row 8 j + 2 (lane % 4) + e % 2.
+__device__ __forceinline__ void sum_adapters(float (&acc)[2][4][4], const GemmArgs& a, int64_t row, int64_t n0,
+                                             int features, int nc, int lane) {
 #pragma unroll
   for (int m = 0; m < 2; m++)
 #pragma unroll
     for (int j = 0; j < 4; j++)
 #pragma unroll
       for (int e = 0; e < 4; e++) acc[m][j][e] = 0.0f;
-  int first = __ffs(firsts) - 1;
-  firsts &= firsts - 1;
-  int32_t cur = __shfl_sync(0xFFFFFFFFu, id, first);
-  int r = 0;
-  load_b(cur, 0, w);
+  int32_t id = lane < nc ? gload(&a.ids[row + lane]) : -1;
+  if (id < 0 || id >= a.adapters) id = -1;
+  const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);
+  const uint32_t all = __ballot_sync(0xFFFFFFFFu, id >= 0 && __ffs(same) - 1 == lane);
+  if (all == 0) return;
+  const uint32_t live = __ballot_sync(0xFFFFFFFFu, id >= 0);
+  const int gr = lane >> 2, q8 = (lane & 3) * 8;
+  const int64_t pitch = static_cast<int64_t>(a.ni) * a.rank;
+  const uint16_t* b = a.b + (n0 + gr) * a.rank + q8;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
-  while (true) {
-    // the step after this one: the next 32 ranks, or the next adapter
-    int32_t nxt = cur;
-    int rn = r + 32;
-    bool more = true;
-    if (rn >= a.rank) {
-      rn = 0;
-      more = firsts != 0;
-      if (more) {
-        nxt = __shfl_sync(0xFFFFFFFFu, id, __ffs(firsts) - 1);
-        firsts &= firsts - 1;
-      }
-    }
-    if (more) load_b(nxt, rn, wn);
-    const uint32_t users = __ballot_sync(0xFFFFFFFFu, id == cur);
+  for (int r = 0; r < a.rank; r += 32) {
+    uint4 w[2][2], wn[2][2];  // features 16 m + 8 h + gr, ranks r + q8 .. + 7
+    auto load_b = [&](int32_t i, uint4(&v)[2][2]) {
+#pragma unroll
+      for (int m = 0; m < 2; m++)
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+          v[m][h] = r + q8 < a.rank && 16 * m + 8 * h + gr < features
+                        ? gload(reinterpret_cast<const uint4*>(b + i * pitch + (16 * m + 8 * h) * a.rank + r))
+                        : zero;
+    };
+    uint32_t firsts = all;
+    int32_t cur = __shfl_sync(0xFFFFFFFFu, id, __ffs(firsts) - 1);
+    firsts &= firsts - 1;
+    load_b(cur, w);
+    float4 u[4][2];  // row 8 j + gr, ranks r + q8 .. + 7
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      if (((users >> (8 * j)) & 0xFF) == 0) continue;
-      float4 u0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u1 = u0;
-      if (((users >> (8 * j + gr)) & 1) && r + q8 < a.rank) {
+      u[j][0] = u[j][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (((live >> (8 * j + gr)) & 1) && r + q8 < a.rank) {
         const float4* up = reinterpret_cast<const float4*>(a.u + (row + 8 * j + gr) * a.rank + r + q8);
-        u0 = gload(up);
-        u1 = gload(up + 1);
+        u[j][0] = gload(up);
+        u[j][1] = gload(up + 1);
       }
-      uint32_t p[4][3];
-      split3(u0.x, u0.y, p[0]);
-      split3(u0.z, u0.w, p[1]);
-      split3(u1.x, u1.y, p[2]);
-      split3(u1.z, u1.w, p[3]);
-#pragma unroll
-      for (int i = 2; i >= 0; i--)
-#pragma unroll
-        for (int m = 0; m < 2; m++) {
-          mma_bf16(acc[m][j], w[m][0].x, w[m][1].x, w[m][0].y, w[m][1].y, p[0][i], p[1][i]);
-          mma_bf16(acc[m][j], w[m][0].z, w[m][1].z, w[m][0].w, w[m][1].w, p[2][i], p[3][i]);
-        }
     }
-    if (!more) break;
-    cur = nxt;
-    r = rn;
+#pragma unroll 1
+    while (true) {
+      const bool more = firsts != 0;
+      const int32_t nxt = __shfl_sync(0xFFFFFFFFu, id, more ? __ffs(firsts) - 1 : 0);
+      firsts &= firsts - 1;
+      if (more) load_b(nxt, wn);
+      const uint32_t users = __ballot_sync(0xFFFFFFFFu, id == cur);
 #pragma unroll
-    for (int m = 0; m < 2; m++)
+      for (int j = 0; j < 4; j++) {
+        if (((users >> (8 * j)) & 0xFF) == 0) continue;
+        const bool mine = (users >> (8 * j + gr)) & 1;
+        const float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const float4 u0 = mine ? u[j][0] : z, u1 = mine ? u[j][1] : z;
+        uint32_t p[4][3];
+        split3(u0.x, u0.y, p[0]);
+        split3(u0.z, u0.w, p[1]);
+        split3(u1.x, u1.y, p[2]);
+        split3(u1.z, u1.w, p[3]);
 #pragma unroll
-      for (int h = 0; h < 2; h++) w[m][h] = wn[m][h];
+        for (int i = 2; i >= 0; i--)
+#pragma unroll
+          for (int m = 0; m < 2; m++) {
+            mma_bf16(acc[m][j], w[m][0].x, w[m][1].x, w[m][0].y, w[m][1].y, p[0][i], p[1][i]);
+            mma_bf16(acc[m][j], w[m][0].z, w[m][1].z, w[m][0].w, w[m][1].w, p[2][i], p[3][i]);
+          }
+      }
+      if (!more) break;
+      cur = nxt;
+#pragma unroll
+      for (int m = 0; m < 2; m++)
+#pragma unroll
+        for (int h = 0; h < 2; h++) w[m][h] = wn[m][h];
+    }
   }
-  // 16 rows at a time: [row][feature], the features' blocks of 8 exchanged by row
-  // pair so that the four row pairs of an instruction lie in different banks
+}
+
+// y2[i] (lane = feature, rows 2i and 2i + 1) += acc, which changes layout in
+// shared memory, 16 rows at a time: [row][feature], the features' blocks of 8
+// exchanged by row pair so that an instruction's four row pairs lie in different banks.
+__device__ __forceinline__ void add_adapters(uint64_t (&y2)[16], uint32_t (&turn)[16][32], const float (&acc)[2][4][4],
+                                             int lane) {
+  const int gr = lane >> 2, q8 = (lane & 3) * 8;
 #pragma unroll
   for (int h = 0; h < 2; h++) {
     __syncwarp();
@@ -961,6 +966,15 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
       // first two; gated: of the up or the gate half)
       constexpr int kChunks = kGated ? 4 : 8, kMine = kChunks / 2;
       auto chunk = [&](int set, int ci) { return (set == 0 ? (ci == 0 ? kChunks - 2 : 2 * (ci - 1)) : 2 * ci) + half; };
+      // first column of a warp's ci-th chunk and its rows (adapters: a tile of a few
+      // rows is cut in two, so that a decode step's adapters are shared out)
+      auto first_col = [&](const GemmTile& t, int set, int ci) {
+        const int c = chunk(set, ci);
+        return kMode == kGemmAdapter && t.jv <= 32 && c < 2 ? c * (((t.jv + 15) >> 4) << 3) : 32 * c;
+      };
+      auto chunk_rows = [&](const GemmTile& t) {
+        return kMode == kGemmAdapter && t.jv <= 32 ? ((t.jv + 15) >> 4) << 3 : 32;
+      };
       // a tile's factors, read before the tile before it is finished
       struct Factors {
         float i, up;
@@ -974,7 +988,7 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
         }
 #pragma unroll
         for (int ci = 0; ci < kMine; ci++) {
-          const int c = chunk(set, ci) * 32 + lane;
+          const int c = first_col(t, set, ci) + lane;
           f.j[ci] = c < t.jv ? gload(&a.j.s2[t.jrow + c]) : 0.0f;
         }
       };
@@ -996,14 +1010,20 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
         const bool live = il < t.iv;
         const int64_t n = t.i0 + il;
         const int set = tiles & 1;
-        if (!empty) {
-          if (!mbar_wait(&sm.acc_full, tiles & 1)) {
-            if (lane == 0) sm.gave_up = 1;
-            break;
+        // the accumulator is waited for when it is first read; every warp waits for
+        // every tile's, or it would take one phase for another
+        bool full = empty, ok = true;
+        auto wait_full = [&] {
+          if (!full) {
+            ok = mbar_wait(&sm.acc_full, tiles & 1);
+            full = true;
+            tc_fence_after();
           }
-          tc_fence_after();
-        }
-        if (kMode == kGemmAdapter) grid_dependency_wait();  // u comes from the kernel before this one
+        };
+        if (kMode == kGemmAdapter)
+          grid_dependency_wait();  // u comes from the kernel before this one
+        else
+          wait_full();
         const uint32_t acc = tmem + (set ? kGAcc1 : 0) + (static_cast<uint32_t>(32 * q) << 16);
         const uint64_t si2 = pack2(f.i, f.i), su2 = pack2(f.up, f.up);
         bool freed = empty;
@@ -1021,11 +1041,19 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
           }
         };
 #pragma unroll 1
-        for (int ci = 0; ci < kMine; ci++) {
-          const int c0 = chunk(set, ci) * 32;
+        for (int ci = 0; ci < kMine && ok; ci++) {
+          const int c0 = first_col(t, set, ci);
           if (c0 >= t.jv) {
             if (ci == 0) release();
             continue;
+          }
+          const int nc = min(chunk_rows(t), t.jv - c0);
+          const int64_t row = t.jrow + c0;
+          const int features = t.iv - 32 * q;
+          float extra[2][4][4];
+          if (kMode == kGemmAdapter) {
+            sum_adapters(extra, a, row, t.i0 + 32 * q, features, nc, lane);
+            wait_full();
           }
           uint32_t v[32], w[32];
           if (empty) {
@@ -1047,8 +1075,6 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
             if (kGated) tmem_load_wait(w);
           }
           if (ci == 0) release();
-          const int nc = min(32, t.jv - c0);
-          const int64_t row = t.jrow + c0;
           uint64_t y[16], z[16];  // rows 2k and 2k + 1
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {
@@ -1061,7 +1087,6 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
               z[k + 1] = mul2x(mul2x(pair2(w[2 * k + 2], w[2 * k + 3]), s1), su2);
             }
           }
-          const int features = t.iv - 32 * q;
           uint32_t b[16];
           if (kGated) {
             if (a.pre != nullptr) {
@@ -1078,7 +1103,7 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
             for (int k = 0; k < 16; k++) b[k] = bf16x2_rn(silu(lo2(y[k])) * lo2(z[k]), silu(hi2(y[k])) * hi2(z[k]));
             store_bf16(b, turn, static_cast<uint16_t*>(a.out) + row * a.ni + t.i0 + 32 * q, a.ni, nc, features, lane);
           } else {
-            if (kMode == kGemmAdapter) add_adapters(y, turn, a, row, t.i0 + 32 * q, features, nc, lane);
+            if (kMode == kGemmAdapter) add_adapters(y, turn, extra, lane);
             if (a.out_f32) {
               float* o = static_cast<float*>(a.out) + row * a.ni + n;
 #pragma unroll
@@ -1092,6 +1117,11 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
               store_bf16(b, turn, static_cast<uint16_t*>(a.out) + row * a.ni + t.i0 + 32 * q, a.ni, nc, features, lane);
             }
           }
+        }
+        wait_full();
+        if (!ok) {
+          if (lane == 0) sm.gave_up = 1;
+          break;
         }
         if (!empty) tiles++;
       }

@@ -874,7 +874,7 @@ nvfp4_status launch_shrink(const ShrinkArgs& s, int sms, cudaStream_t stream) {
   // adapters side by side and K over a cluster while that fills the GPU
   int slots = 1, cn = 1;
   while (slots < kTok && slots < s.adapters && blocks * slots < sms) slots *= 2;
-  while (cn < 8 && blocks * slots * cn < 2 * sms && (s.K + 31) / 32 >= 16 * cn) cn *= 2;
+  while (cn < 8 && blocks * slots * cn <= (kMT == 1 ? sms : 2 * sms) && (s.K + 31) / 32 >= 16 * cn) cn *= 2;
   auto kernel = adapter_shrink_kernel<kMT, kNT>;
   const size_t smem = static_cast<size_t>(8) * kTok * 8 * kNT * 4;
   if (smem > 46 * 1024 &&
