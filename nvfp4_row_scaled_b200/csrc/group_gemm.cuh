@@ -41,12 +41,12 @@
 //   warp 1      tensor memory, scale copies shared -> tensor memory, MMAs (in
 //               a pair the first CTA's; the second's passes on that its stage
 //               has been filled)
-//   warps 2-5   what TMA cannot address, a stage to a warp: row-major block
+//   warps 4-7   what TMA cannot address, a stage to a warp: row-major block
 //               scales (16 bytes a row and k block, read ahead into registers
 //               and written as the 128x4 tiles the MMA wants) and, with kTma =
 //               false, the codes themselves (row strides that are not
 //               multiples of 16 bytes; wgrad's per-group strides)
-//   warps 6-13  epilogue: two warps for each 32-lane quarter, alternate
+//   warps 8-15  epilogue: two warps for each 32-lane quarter, alternate
 //               32-column chunks
 // Tensor memory holds two 256-column accumulators at columns 0 and 192 that
 // share 64 columns, and 48 columns of scales behind them: the next tile's
@@ -69,10 +69,16 @@ namespace nvfp4rs {
 
 enum GemmMode : int { kGemmPlain = 0, kGemmGated = 1, kGemmWgrad = 2, kGemmAdapter = 3 };
 
-constexpr int kGThreads = 448;       // 1 TMA + 1 MMA + 4 loader + 8 epilogue warps
-constexpr int kGLoadWarp = 2;
-constexpr int kGEpiWarp = 6;
+constexpr int kGThreads = 512;       // warpgroups: TMA and MMA warps (two idle), loaders, 2 of epilogue
+constexpr int kGLoadWarp = 4;
+constexpr int kGEpiWarp = 8;
 constexpr int kGEpiWarps = 8;
+// registers a thread: 128 at launch; the first warpgroup gives 64 of them up and
+// the two of the epilogue take 32 each (the loaders keep theirs)
+constexpr int kGRegsLaunch = 65536 / kGThreads, kGRegsIssue = 64, kGRegsEpi = 160;
+static_assert(kGRegsIssue <= kGRegsLaunch && kGRegsEpi >= kGRegsLaunch &&
+                  kGRegsIssue + kGRegsLaunch + 2 * kGRegsEpi <= 4 * kGRegsLaunch,
+              "register split");
 constexpr int kGI = 128;             // I rows (accumulator lanes) of a CTA's tile
 constexpr int kGK = 256;             // contraction elements of a stage: 128 bytes a row
 constexpr int kGBigJ = 128;          // J rows of a TMA box ...
@@ -110,7 +116,7 @@ struct GemmArgs {
   int32_t jt, jt_log;       // J rows of a tile: a power of two, 16 to 256; its logarithm
   uint32_t it, it_magic;    // I tiles of a group; floor(2^32 / it), 2^32 - 1 for it = 1
   int32_t jbulk;     // nonzero: J scales by bulk copies (tiled, and J tiles of whole 128-row blocks)
-  int32_t loaders;   // nonzero: warps 2-5 take part
+  int32_t loaders;   // nonzero: warps 4-7 take part
   int32_t producer;  // nonzero: warp 0 takes part
   int32_t out_f32;
   void* out;         // [J rows][ni]
@@ -702,8 +708,11 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sm.tmem);
 
-  if (sm.routing.ok) {
-    if (warp == 0 && a.producer) {
+  if (warp < kGLoadWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGRegsIssue));
+    if (!sm.routing.ok) {
+      // nothing to do
+    } else if (warp == 0 && a.producer) {
       Walk walk(sm.routing, a);
       GemmTile t;
       const bool elected = elect_one();
@@ -826,7 +835,9 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
         __syncwarp();
         mbar_wait(&sm.drain, 0);
       }
-    } else if (warp >= kGLoadWarp && warp < kGEpiWarp && a.loaders) {
+    }
+  } else if (warp < kGEpiWarp) {
+    if (sm.routing.ok && a.loaders) {
       // Each of the four warps fills every fourth stage by itself, so that four
       // stages' latencies overlap.
       GemmBlocks<kMode, kPair> at(sm.routing, a);
@@ -957,7 +968,10 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
       }
       cp_async_wait<0>();
       if (!ok) sm.gave_up = 1;
-    } else if (warp >= kGEpiWarp) {
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGRegsEpi));
+    if (sm.routing.ok) {
       const int q = warp & 3;                       // accumulator lanes 32q .. 32q+31
       const int half = (warp - kGEpiWarp) >> 2;     // chunks of parity `half`
       const int il = 32 * q + lane;
