@@ -387,8 +387,8 @@ NVFP4RS_API nvfp4_status nvfp4_mx_dequantize(const uint8_t* data, const uint8_t*
  *
  * Requirements (else NVFP4_ERR_INVALID_ARG): every width that is a block
  * dimension of the cast is a multiple of 16 (K, N, F). Else
- * NVFP4_ERR_UNSUPPORTED: pointers 16-byte aligned (s2: 4), stacked weight
- * rows < 2^31, and with NVFP4_SCALE_TILED_128X4 an operand whose matrices are
+ * NVFP4_ERR_UNSUPPORTED: pointers 16-byte aligned (s2: 4), rows and stacked
+ * weight rows up to 2^31 - 1024, K and N up to 2^30, and with NVFP4_SCALE_TILED_128X4 an operand whose matrices are
  * multiples of 128 rows and of 128 columns (so 128-row groups for x).
  * With row-major (compact) scales groups may have any number of rows, 0 and
  * 1 included. K % 32 == 0 takes the faster load path. Buffers must not overlap

@@ -105,7 +105,8 @@ struct GemmOperand {
   const uint8_t* data;
   const uint8_t* scale;
   const float* s2;
-  int32_t tiled;  // block scales in 128x4 tiles
+  int32_t tiled;       // block scales in 128x4 tiles
+  const uint8_t* end;  // behind the last block scale
 };
 
 struct GemmArgs {
@@ -424,10 +425,10 @@ __device__ __forceinline__ void load_codes(uint32_t dst, const uint8_t* data, in
 // 128x4 tiles.
 enum ScaleRead : int { kRead16 = 0, kReadWords = 1, kReadBytes = 2, kReadTiled = 3 };
 
-// `left`: scales from p to the row's end. What is read raw is put together by
-// scale_words() later, so that a read is not waited for here. A stacked matrix
-// ends on a 16-byte boundary: a word that holds a byte of it lies inside it.
-__device__ __forceinline__ void read_scales(const uint8_t* p, int how, int32_t left, uint32_t (&w)[5]) {
+// `left`: scales from p to the row's end; `end`: behind the last scale of the
+// stacked matrix. What is read raw is put together by scale_words() later, so
+// that a read is not waited for here.
+__device__ __forceinline__ void read_scales(const uint8_t* p, int how, int32_t left, const uint8_t* end, uint32_t (&w)[5]) {
 #pragma unroll
   for (int k = 0; k < 5; k++) w[k] = 0u;
   if (p == nullptr) return;
@@ -440,8 +441,16 @@ __device__ __forceinline__ void read_scales(const uint8_t* p, int how, int32_t l
   } else if (how == kReadBytes) {
     const int b = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 3);
 #pragma unroll
-    for (int k = 0; k < 5; k++)
-      if (4 * k < left + b) w[k] = gload(reinterpret_cast<const uint32_t*>(p - b) + k);
+    for (int k = 0; k < 5; k++) {
+      const uint8_t* q = p - b + 4 * k;  // before p: bytes of the row before, in the matrix, which starts on 16 bytes
+      if (4 * k < left + b) {
+        if (q + 4 <= end) {
+          w[k] = gload(reinterpret_cast<const uint32_t*>(q));
+        } else {  // the matrix ends inside the word
+          for (int e = 0; q + e < end; e++) w[k] |= static_cast<uint32_t>(gload(q + e)) << (8 * e);
+        }
+      }
+    }
   } else {
     const int step = how == kReadTiled ? kGScaleTile / 4 : 1;
 #pragma unroll
@@ -517,15 +526,17 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t (&p)[3]) {
 
 // The adapters' share of a warp's 32 features x 32 rows (features n0 .., rows
 // row .. row + nc - 1): sum_r u[row][r] b[id][n][r], on the bf16 tensor cores, 16
-// features x 8 rows x 16 ranks an instruction. u is fp32 and stays so: three bf16
-// terms of it multiply b and meet in the fp32 accumulator. Each distinct adapter
+// features x 8 rows x 16 ranks an instruction. u is fp32: three bf16 terms of it
+// (2^-25 of u) multiply b and meet in the fp32 accumulator; a bf16 result, whose
+// own rounding is 2^-8, takes two (2^-17). Each distinct adapter
 // of the rows is one pass over the 8-row blocks that use it, with the other
 // rows' u as zeros -- which add nothing, so a row's result does not depend on
 // its neighbours; the next pass's b is loaded meanwhile. The ranks are numbered as a
 // lane loads them (8 of a row, 16 bytes), alike on both sides. Reads nothing of
 // the projection, so a tile's first chunk is summed while the tile is still being
-// multiplied. (In fp32 FMAs, 8 ranks x 32 rows a step, this took 60 k cycles of
-// a 128 x 256 tile's epilogue at rank 32.)
+// multiplied. What bounds it: these instructions wait behind the projection's
+// tcgen05 ones, about 100 cycles each, so the fewer the better. In fp32 FMAs, with
+// u read from shared memory, 8192 rows at rank 32 took 191 us against 142.
 // acc[m][j][e]: feature 16 m + 8 (e / 2) + lane / 4, row 8 j + 2 (lane % 4) + e % 2.
 __device__ __forceinline__ void sum_adapters(float (&acc)[2][4][4], const GemmArgs& a, int64_t row, int64_t n0,
                                              int features, int nc, int lane) {
@@ -590,12 +601,14 @@ __device__ __forceinline__ void sum_adapters(float (&acc)[2][4][4], const GemmAr
         split3(u1.x, u1.y, p[2]);
         split3(u1.z, u1.w, p[3]);
 #pragma unroll
-        for (int i = 2; i >= 0; i--)
+        for (int i = 2; i >= 0; i--) {
+          if (i == 2 && !a.out_f32) continue;
 #pragma unroll
           for (int m = 0; m < 2; m++) {
             mma_bf16(acc[m][j], w[m][0].x, w[m][1].x, w[m][0].y, w[m][1].y, p[0][i], p[1][i]);
             mma_bf16(acc[m][j], w[m][0].z, w[m][1].z, w[m][0].w, w[m][1].w, p[2][i], p[3][i]);
           }
+        }
       }
       if (!more) break;
       cur = nxt;
@@ -758,7 +771,7 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
                             jy + big * kGBigJ + b * kGBoxJ, bar, pol);
             }
             uint8_t* sf = st + Stage::kData;
-            const int32_t so = kb * 4 * kGScaleTile;
+            const int64_t so = static_cast<int64_t>(kb) * 4 * kGScaleTile;
             if (a.i.tiled) {
               bulk_load(sf, is + so, sf_bytes, bar);
               if (kGated) bulk_load(sf + 4 * kGScaleTile, is + a.ni / 128 * kt * kGScaleTile + so, sf_bytes, bar);
@@ -861,8 +874,8 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
           for (int e = 0; e < 4; e++) {
             const bool in = lane + 32 * e < t.iv;
             const uint8_t* pe = p + static_cast<int64_t>(32 * e) * cols;
-            read_scales(in ? pe : nullptr, how, left, r.w[0][e]);
-            if (kGated) read_scales(in ? pe + static_cast<int64_t>(a.ni) * cols : nullptr, how, left, r.w[1][e]);
+            read_scales(in ? pe : nullptr, how, left, a.i.end, r.w[0][e]);
+            if (kGated) read_scales(in ? pe + static_cast<int64_t>(a.ni) * cols : nullptr, how, left, a.i.end, r.w[1][e]);
           }
         }
         if (!a.jbulk) {
@@ -880,7 +893,7 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
                      (jr & 31) * 16 + ((jr & 127) >> 5) * 4;
               else
                 pe = a.j.scale + jb + static_cast<int64_t>(jr) * cols + first;
-              read_scales(j < t.jv ? pe : nullptr, a.j.tiled ? kReadTiled : how, left, r.w[kJ + h][e]);
+              read_scales(j < t.jv ? pe : nullptr, a.j.tiled ? kReadTiled : how, left, a.j.end, r.w[kJ + h][e]);
             }
           }
         }

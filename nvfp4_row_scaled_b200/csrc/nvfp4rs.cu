@@ -35,6 +35,7 @@ using namespace nvfp4rs;
 namespace {
 
 constexpr int64_t kMaxRows = (int64_t{1} << 31) - kRows;
+constexpr int64_t kMaxProductRows = (int64_t{1} << 31) - 1024;  // a tile may reach past the last row in int32
 constexpr int kMxBlock = 32;  // MXFP4 block: 32 elements along K (rowwise) and along a group's rows (colwise)
 constexpr int kMaxAmaxCols = 32768;  // columns per amax CTA (dynamic shared memory)
 
@@ -602,8 +603,8 @@ nvfp4_status check_product(int64_t rows, int64_t K, int32_t E, int64_t n_rows, c
   if (K % 16 != 0 || n_rows % 16 != 0) return NVFP4_ERR_INVALID_ARG;
   if (rows > 0 && n_rows > 0 && out == nullptr) return NVFP4_ERR_INVALID_ARG;
   constexpr int64_t kMaxDim = int64_t{1} << 30;
-  if (E > NVFP4_MAX_GROUPS || rows > kMaxRows || K > kMaxDim || n_rows > kMaxDim) return NVFP4_ERR_UNSUPPORTED;
-  if (n_rows > 0 && E > kMaxRows / n_rows) return NVFP4_ERR_UNSUPPORTED;
+  if (E > NVFP4_MAX_GROUPS || rows > kMaxProductRows || K > kMaxDim || n_rows > kMaxDim) return NVFP4_ERR_UNSUPPORTED;
+  if (n_rows > 0 && E > kMaxProductRows / n_rows) return NVFP4_ERR_UNSUPPORTED;
   if (!aligned(out, 16)) return NVFP4_ERR_UNSUPPORTED;
   return NVFP4_OK;
 }
@@ -707,6 +708,8 @@ nvfp4_status launch_gemm(const Routing& routing, GemmArgs a, int64_t rows, int64
   a.it = static_cast<uint32_t>(pair ? it2 : it1);
   a.it_magic = a.it == 1 ? 0xFFFFFFFFu : static_cast<uint32_t>((uint64_t{1} << 32) / a.it);
   const bool tma = !kWgrad && a.K % 32 == 0 && a.K > 0;
+  a.i.end = a.i.scale + (kWgrad ? rows * a.ni : i_rows * a.K) / 16;
+  a.j.end = a.j.scale + (kWgrad ? rows * a.nj : j_rows * a.K) / 16;
   a.jbulk = a.j.tiled && a.jt % kRows == 0;
   a.loaders = !tma || !a.i.tiled || !a.jbulk;
   a.producer = tma || a.i.tiled || a.jbulk;
@@ -742,7 +745,7 @@ nvfp4_status launch_gemm(const Routing& routing, GemmArgs a, int64_t rows, int64
 }
 
 GemmOperand operand(const nvfp4_matrix* m) {
-  return GemmOperand{m->data, m->scale, m->s2, m->scale_layout == NVFP4_SCALE_TILED_128X4};
+  return GemmOperand{m->data, m->scale, m->s2, m->scale_layout == NVFP4_SCALE_TILED_128X4, nullptr};
 }
 
 nvfp4_status check_gemm(const nvfp4_matrix* x, int64_t rows, int64_t K, int32_t E, const nvfp4_matrix* w, int64_t n_rows,
