@@ -1037,23 +1037,9 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
         const bool live = il < t.iv;
         const int64_t n = t.i0 + il;
         const int set = tiles & 1;
-        // the accumulator is waited for when it is first read; every warp waits for
-        // every tile's, or it would take one phase for another
-        bool full = empty, ok = true;
-        auto wait_full = [&] {
-          if (!full) {
-            ok = mbar_wait(&sm.acc_full, tiles & 1);
-            full = true;
-            tc_fence_after();
-          }
-        };
-        if (kMode == kGemmAdapter)
-          grid_dependency_wait();  // u comes from the kernel before this one
-        else
-          wait_full();
         const uint32_t acc = tmem + (set ? kGAcc1 : 0) + (static_cast<uint32_t>(32 * q) << 16);
         const uint64_t si2 = pack2(f.i, f.i), su2 = pack2(f.up, f.up);
-        bool freed = empty;
+        bool freed = empty, full = empty, ok = true, no_shared = false;
         auto release = [&] {
           if (!freed) {
             tc_fence_before();
@@ -1067,11 +1053,32 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
             freed = true;
           }
         };
+        // The accumulator is waited for when it is first read. Every warp waits for
+        // every tile's, and frees the shared columns only after that: freed
+        // before, the next tile's MMAs could complete a second phase of acc_full,
+        // and a warp that still waits for this one's would wait for good.
+        auto wait_full = [&] {
+          if (!full) {
+            ok = mbar_wait(&sm.acc_full, tiles & 1);
+            full = true;
+            tc_fence_after();
+            if (no_shared) release();
+          }
+        };
+        if (kMode == kGemmAdapter)
+          grid_dependency_wait();  // u comes from the kernel before this one
+        else
+          wait_full();
 #pragma unroll 1
         for (int ci = 0; ci < kMine && ok; ci++) {
           const int c0 = first_col(t, set, ci);
           if (c0 >= t.jv) {
-            if (ci == 0) release();
+            if (ci == 0) {  // no columns of this warp's among the shared ones
+              if (full)
+                release();
+              else
+                no_shared = true;
+            }
             continue;
           }
           const int nc = min(chunk_rows(t), t.jv - c0);

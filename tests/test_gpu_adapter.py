@@ -83,6 +83,17 @@ def test_adapters(rows, K, N, R, L, kind):
     check(y, *reference(c), f"{rows} {K} {N} {R} {L} {kind}")
 
 
+@pytest.mark.parametrize("rows,K,N,L", [(238, 512, 1760, 20), (100, 256, 4096, 7), (600, 1024, 8192, 3), (37, 64, 8192, 37)])
+@pytest.mark.parametrize("kind", ["each", "runs", "none"])
+def test_many_small_tiles_a_cta(rows, K, N, L, kind):
+    """More tiles than SMs, of fewer rows than the columns that two accumulators share."""
+    c = case(rows, K, N, 16, L, spread(rows, L, kind), rows + N)
+    for _ in range(3):
+        y, st = run(c)
+        assert st == 0
+    check(y, *reference(c), f"{rows} {K} {N} {L} {kind}")
+
+
 @pytest.mark.parametrize("R", [8, 32, 48, 56, 64])
 def test_fp32_and_every_rank(R):
     c = case(40, 320, 48, R, 4, spread(40, 4, "mixed"), R)
