@@ -708,8 +708,6 @@ nvfp4_status launch_gemm(const Routing& routing, GemmArgs a, int64_t rows, int64
   a.it = static_cast<uint32_t>(pair ? it2 : it1);
   a.it_magic = a.it == 1 ? 0xFFFFFFFFu : static_cast<uint32_t>((uint64_t{1} << 32) / a.it);
   const bool tma = !kWgrad && a.K % 32 == 0 && a.K > 0;
-  a.i.end = a.i.scale + (kWgrad ? rows * a.ni : i_rows * a.K) / 16;
-  a.j.end = a.j.scale + (kWgrad ? rows * a.nj : j_rows * a.K) / 16;
   a.jbulk = a.j.tiled && a.jt % kRows == 0;
   a.loaders = !tma || !a.i.tiled || !a.jbulk;
   a.producer = tma || a.i.tiled || a.jbulk;
@@ -721,8 +719,8 @@ nvfp4_status launch_gemm(const Routing& routing, GemmArgs a, int64_t rows, int64
     NVFP4_SPANS(SpanList{}
                     .add(a.j.data, jb / 2, false)
                     .add(a.i.data, ib / 2, false)
-                    .add(a.i.scale, ib / 16, false)
-                    .add(a.j.scale, jb / 16, false)
+                    .add(a.i.scale, (ib / 16 + 3) & ~size_t{3}, false)  // whole aligned words
+                    .add(a.j.scale, (jb / 16 + 3) & ~size_t{3}, false)
                     .add(a.i.s2, 4 * static_cast<size_t>(i_rows), false)
                     .add(a.j.s2, 4 * static_cast<size_t>(j_rows), false)
                     .routing(routing)
@@ -745,7 +743,7 @@ nvfp4_status launch_gemm(const Routing& routing, GemmArgs a, int64_t rows, int64
 }
 
 GemmOperand operand(const nvfp4_matrix* m) {
-  return GemmOperand{m->data, m->scale, m->s2, m->scale_layout == NVFP4_SCALE_TILED_128X4, nullptr};
+  return GemmOperand{m->data, m->scale, m->s2, m->scale_layout == NVFP4_SCALE_TILED_128X4};
 }
 
 nvfp4_status check_gemm(const nvfp4_matrix* x, int64_t rows, int64_t K, int32_t E, const nvfp4_matrix* w, int64_t n_rows,
