@@ -326,3 +326,28 @@ def test_offsets_past_32_bits():
     y = torch.empty(5, N, device="cuda")
     abi.nvfp4_group_gemm(x, [0] * (E - 1) + [5], rep, y)
     check(y, *product(xv, wlv))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_do_not_depend_on_the_size_of_the_call(dtype):
+    """The same bits from a call large enough for pairs of CTAs, from a few rows and
+    from one."""
+    K, N, rows = 1056, 2064, 4100
+    x, xv = random_matrix(rows, K, 26)
+    w, wv = random_matrix(N, K, 27)
+    y = torch.empty(rows, N, dtype=dtype, device="cuda")
+    abi.nvfp4_group_gemm(x, [rows], w, y)
+    check(y[-300:], *product(xv[-300:], wv), "large")
+    for lo, hi in ((0, 1), (7, 60), (4000, 4100)):
+        part = abi.matrix(*(x[k][lo:hi].clone() for k in ("data", "scale", "s2")))  # 16-byte aligned copies
+        z = torch.empty(hi - lo, N, dtype=dtype, device="cuda")
+        abi.nvfp4_group_gemm(part, [hi - lo], w, z)
+        assert torch.equal(z, y[lo:hi]), (lo, hi)
+
+
+def test_large_gated_and_wgrad_pairs():
+    """Pairs of CTAs with ragged ends on both sides, empty groups among them."""
+    m, K, F = [700, 0, 1, 900, 333], 544, 1040
+    run_gated(m, K, F, COMPACT, True)
+    run_wgrad([304, 0, 512, 16], 1552, 1296, torch.bfloat16, COMPACT, COMPACT)
+    run_wgrad([256, 0, 512], 1536, 1280, torch.float32, TILED, TILED)
