@@ -798,7 +798,7 @@ nvfp4_status launch_gated_backward(const Routing& routing, const void* dh, const
   const int64_t n_col = col_amax != nullptr ? 2 * F * routing.E : 0;
   const int64_t tiles = (rows + kBwRows - 1) / kBwRows;
   if (n_col == 0 && tiles == 0) return NVFP4_OK;
-  const size_t n = static_cast<size_t>(rows) * static_cast<size_t>(F);
+  [[maybe_unused]] const size_t n = static_cast<size_t>(rows) * static_cast<size_t>(F);
   NVFP4_SPANS(SpanList{}
                   .add(dh, 2 * n, false)
                   .add(gate_up, 4 * n, false)
