@@ -528,16 +528,19 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t (&p)[3]) {
 // (2^-25 of u) multiply b and meet in the fp32 accumulator; a bf16 result, whose
 // own rounding is 2^-8, takes two (2^-17). Each distinct adapter
 // of the rows is one pass over the 8-row blocks that use it, with the other
-// rows' u as zeros -- which add nothing, so a row's result does not depend on
-// its neighbours; the next pass's b is loaded meanwhile. The ranks are numbered as a
+// rows' u as zeros -- which add nothing while b is finite, so a row's result does not
+// depend on its neighbours; the next pass's b is loaded meanwhile. A pass whose b
+// (these features, these ranks) holds an infinity or NaN, which 0 would not cancel,
+// is left out and its rows are returned in `slow`, their sums zero: add_slow() sums them. The ranks are numbered as a
 // lane loads them (8 of a row, 16 bytes), alike on both sides. Reads nothing of
 // the projection, so a tile's first chunk is summed while the tile is still being
 // multiplied. What bounds it: these instructions wait behind the projection's
 // tcgen05 ones, about 100 cycles each, so the fewer the better. In fp32 FMAs, with
 // u read from shared memory, 8192 rows at rank 32 took 191 us against 142.
 // acc[m][j][e]: feature 16 m + 8 (e / 2) + lane / 4, row 8 j + 2 (lane % 4) + e % 2.
-__device__ __forceinline__ void sum_adapters(float (&acc)[2][4][4], const GemmArgs& a, int64_t row, int64_t n0,
-                                             int features, int nc, int lane) {
+__device__ __forceinline__ void sum_adapters(float (&acc)[2][4][4], uint32_t& slow, const GemmArgs& a, int64_t row,
+                                             int64_t n0, int features, int nc, int lane) {
+  slow = 0;
 #pragma unroll
   for (int m = 0; m < 2; m++)
 #pragma unroll
@@ -587,9 +590,18 @@ __device__ __forceinline__ void sum_adapters(float (&acc)[2][4][4], const GemmAr
       firsts &= firsts - 1;
       if (more) load_b(nxt, wn);
       const uint32_t users = __ballot_sync(0xFFFFFFFFu, id == cur);
+      uint32_t top = 0;  // the largest exponent and mantissa of each half word
+#pragma unroll
+      for (int m = 0; m < 2; m++)
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+          top = umax2(umax2(umax2(top, w[m][h].x & 0x7FFF7FFFu), umax2(w[m][h].y & 0x7FFF7FFFu, w[m][h].z & 0x7FFF7FFFu)),
+                      w[m][h].w & 0x7FFF7FFFu);
+      const bool finite = !__any_sync(0xFFFFFFFFu, (top & 0xFFFFu) >= 0x7F80u || top >= 0x7F800000u);
+      if (!finite) slow |= users;
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        if (((users >> (8 * j)) & 0xFF) == 0) continue;
+        if (!finite || ((users >> (8 * j)) & 0xFF) == 0) continue;
         const bool mine = (users >> (8 * j + gr)) & 1;
         const float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         const float4 u0 = mine ? u[j][0] : z, u1 = mine ? u[j][1] : z;
@@ -616,6 +628,15 @@ __device__ __forceinline__ void sum_adapters(float (&acc)[2][4][4], const GemmAr
         for (int h = 0; h < 2; h++) w[m][h] = wn[m][h];
     }
   }
+  if (slow) {
+#pragma unroll
+    for (int m = 0; m < 2; m++)
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+          if ((slow >> (8 * j + 2 * (lane & 3) + (e & 1))) & 1) acc[m][j][e] = 0.0f;
+  }
 }
 
 // y2[i] (lane = feature, rows 2i and 2i + 1) += acc, which changes layout in
@@ -640,6 +661,35 @@ __device__ __forceinline__ void add_adapters(uint64_t (&y2)[16], uint32_t (&turn
       const int f = lane ^ ((k & 3) << 3);
       uint64_t& y = y2[8 * h + k];
       y = pack2(lo2(y) + __uint_as_float(turn[2 * k][f]), hi2(y) + __uint_as_float(turn[2 * k + 1][f]));
+    }
+  }
+}
+
+// The rows that sum_adapters() left out, y2 as there: fp32 FMAs in the order of the ranks,
+// a lane a feature. Infinities and NaN come out as the formula has them; the
+// rows' finite results are exact to the FMAs' roundings. The other rows add -0.
+__device__ __forceinline__ void add_slow(uint64_t (&y2)[16], uint32_t (&turn)[16][32], uint32_t slow, const GemmArgs& a,
+                                         int64_t row, int64_t n, bool live, int lane) {
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; i++) turn[i][lane] = 0x80000000u;
+    for (uint32_t left = (slow >> (16 * h)) & 0xFFFFu; left != 0; left &= left - 1) {
+      const int i = __ffs(left) - 1;
+      const int64_t t = row + 16 * h + i, id = gload(&a.ids[t]);
+      const float* u = a.u + t * a.rank;
+      const uint16_t* b = a.b + (id * a.ni + n) * a.rank;
+      float s = 0.0f;
+#pragma unroll 1
+      for (int r = 0; live && r < a.rank; r++)
+        s = __fmaf_rn(gload(u + r), __uint_as_float(static_cast<uint32_t>(gload(b + r)) << 16), s);
+      turn[i][lane] = __float_as_uint(s);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      uint64_t& y = y2[8 * h + k];
+      y = pack2(lo2(y) + __uint_as_float(turn[2 * k][lane]), hi2(y) + __uint_as_float(turn[2 * k + 1][lane]));
     }
   }
 }
@@ -1083,8 +1133,9 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
           const int64_t row = t.jrow + c0;
           const int features = t.iv - 32 * q;
           float extra[2][4][4];
+          uint32_t slow = 0;
           if (kMode == kGemmAdapter) {
-            sum_adapters(extra, a, row, t.i0 + 32 * q, features, nc, lane);
+            sum_adapters(extra, slow, a, row, t.i0 + 32 * q, features, nc, lane);
             wait_full();
           }
           uint32_t v[32], w[32];
@@ -1135,7 +1186,10 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
             for (int k = 0; k < 16; k++) b[k] = bf16x2_rn(silu(lo2(y[k])) * lo2(z[k]), silu(hi2(y[k])) * hi2(z[k]));
             store_bf16(b, turn, static_cast<uint16_t*>(a.out) + row * a.ni + t.i0 + 32 * q, a.ni, nc, features, lane);
           } else {
-            if (kMode == kGemmAdapter) add_adapters(y, turn, extra, lane);
+            if (kMode == kGemmAdapter) {
+              add_adapters(y, turn, extra, lane);
+              if (slow != 0) add_slow(y, turn, slow, a, row, n, live, lane);
+            }
             if (a.out_f32) {
               float* o = static_cast<float*>(a.out) + row * a.ni + n;
 #pragma unroll

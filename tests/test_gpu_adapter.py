@@ -176,3 +176,45 @@ def test_graph_replays_with_other_ids():
         torch.cuda.synchronize()
         assert int(st.item()) == 0
         check(y, *reference(c), kind)
+
+
+def neighbours_case(seed, rows=70, L=5, K=256, N=96, R=40, kind="each"):
+    return case(rows, K, N, R, L, spread(rows, L, kind), seed)
+
+
+def non_finite(part, bad, kind, dtype):
+    """Tokens of the other adapters, or of none, keep the bits that they have beside a
+    finite adapter; the adapter's own tokens get what the formula gives."""
+    c = neighbours_case(40, kind=kind)
+    clean, _ = run(c, dtype)
+    i, n, r, k = 2, 37, 35, 100
+    own = c["ids"].cpu() == i
+    assert 3 < int(own.sum()) < 40
+    d = dict(c)
+    d[part] = c[part].clone()
+    d[part][{"a": (i, r, k), "b": (i, n, r), "f": (i,)}[part]] = bad
+    y, st = run(d, dtype)
+    assert st == 0
+    assert torch.equal(y[~own.cuda()], clean[~own.cuda()])
+    # the formula in fp64: which results are infinite (and with which sign), which are NaN
+    p, _ = product(c["xv"], c["wv"])
+    a, b, f, xb = (d[q].double().cpu() for q in ("a", "b", "f", "xb"))
+    want = p[own] + (f[i] * (xb[own] @ a[i].t())) @ b[i].t()
+    got = y.cpu()[own].double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.isinf(got), torch.isinf(want)) and torch.equal(got[torch.isinf(want)], want[torch.isinf(want)])
+    # its finite results are those of the finite adapter: the changed element of b is not in them
+    keep = torch.arange(y.shape[1]) != n
+    if part == "b":
+        ref, lim = reference(c)
+        check(y.cpu()[own][:, keep], ref[own][:, keep], lim[own][:, keep], "finite features")
+
+
+BAD = [float("inf"), float("-inf"), float("nan")]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("kind", ["each", "mixed"])
+@pytest.mark.parametrize("bad", BAD)
+def test_non_finite_b_stays_in_its_tokens(bad, kind, dtype):
+    non_finite("b", bad, kind, dtype)
