@@ -511,6 +511,8 @@ __device__ __forceinline__ void store_bf16(const uint32_t (&y)[16], uint32_t (&t
   }
 }
 
+constexpr float kBf16Round = 0x1.ffp+127f;  // the smallest value that bf16 rounds to infinity
+
 // Three bf16 pairs whose sum is two fp32 values to 2^-25 of each: rounded, the
 // rest rounded, the rest of that.
 __device__ __forceinline__ void split3(float a, float b, uint32_t (&p)[3]) {
@@ -531,7 +533,8 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t (&p)[3]) {
 // rows' u as zeros -- which add nothing while b is finite, so a row's result does not
 // depend on its neighbours; the next pass's b is loaded meanwhile. A pass whose b
 // (these features, these ranks) holds an infinity or NaN, which 0 would not cancel,
-// is left out and its rows are returned in `slow`, their sums zero: add_slow() sums them. The ranks are numbered as a
+// is left out, and so is a row whose u holds an infinity or a value that bf16 rounds to
+// one (split3 would give inf - inf; a NaN stays one): `slow` returns those rows, their sums zero, for add_slow(). The ranks are numbered as a
 // lane loads them (8 of a row, 16 bytes), alike on both sides. Reads nothing of
 // the projection, so a tile's first chunk is summed while the tile is still being
 // multiplied. What bounds it: these instructions wait behind the projection's
@@ -574,6 +577,7 @@ __device__ __forceinline__ void sum_adapters(float (&acc)[2][4][4], uint32_t& sl
     firsts &= firsts - 1;
     load_b(cur, w);
     float4 u[4][2];  // row 8 j + gr, ranks r + q8 .. + 7
+    float largest = 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
       u[j][0] = u[j][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -581,6 +585,24 @@ __device__ __forceinline__ void sum_adapters(float (&acc)[2][4][4], uint32_t& sl
         const float4* up = reinterpret_cast<const float4*>(a.u + (row + 8 * j + gr) * a.rank + r + q8);
         u[j][0] = gload(up);
         u[j][1] = gload(up + 1);
+      }
+      largest = fmaxf(largest, fmaxf(fmaxf(fmaxf(fabsf(u[j][0].x), fabsf(u[j][0].y)), fmaxf(fabsf(u[j][0].z), fabsf(u[j][0].w))),
+                                     fmaxf(fmaxf(fabsf(u[j][1].x), fabsf(u[j][1].y)), fmaxf(fabsf(u[j][1].z), fabsf(u[j][1].w)))));
+    }
+    if (__any_sync(0xFFFFFFFFu, largest >= kBf16Round)) {
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        bool high = false;
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+          high = high || fabsf(u[j][h].x) >= kBf16Round || fabsf(u[j][h].y) >= kBf16Round || fabsf(u[j][h].z) >= kBf16Round ||
+                 fabsf(u[j][h].w) >= kBf16Round;
+        uint32_t rows = __ballot_sync(0xFFFFFFFFu, high);  // lane 4 gr + q: row gr
+        rows |= rows >> 1;
+        rows |= rows >> 2;  // bit 4 gr: any of the row's four lanes
+        if ((rows >> (lane & 28)) & 1) u[j][0] = u[j][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < 8; k++) slow |= ((rows >> (4 * k)) & 1u) << (8 * j + k);
       }
     }
 #pragma unroll 1

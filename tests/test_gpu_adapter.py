@@ -218,3 +218,37 @@ BAD = [float("inf"), float("-inf"), float("nan")]
 @pytest.mark.parametrize("bad", BAD)
 def test_non_finite_b_stays_in_its_tokens(bad, kind, dtype):
     non_finite("b", bad, kind, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("kind", ["each", "mixed"])
+@pytest.mark.parametrize("part", ["a", "f"])
+@pytest.mark.parametrize("bad", BAD)
+def test_non_finite_u(part, bad, kind, dtype):
+    """An infinity or NaN in a or in the factor, so in u."""
+    non_finite(part, bad, kind, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("kind", ["one", "mixed"])
+def test_u_above_the_largest_bf16(kind, dtype):
+    """u = 2^127 (2 - 2^-9): finite in fp32, and above 2^127 (2 - 2^-8), from where bf16
+    rounds to infinity. The tokens beside it, of the same adapter too, keep their bits."""
+    c = case(9, 64, 48, 8, 2, spread(9, 2, kind), 11)
+    t = 4
+    i = int(c["ids"][t])
+    assert i >= 0
+    c["b"] *= 2.0 ** -100
+    c["xb"][:, 5] = 0.5
+    c["a"][i, 3, 5] = 2.0 ** 63
+    c["f"][i] = 2 - 2.0 ** -9
+    base, _ = run(c, dtype)
+    c["xb"][t] = 0
+    c["xb"][t, 5] = 2.0 ** 64
+    y, st = run(c, dtype)
+    assert st == 0
+    u = c["f"][i].double() * 2.0 ** 127
+    assert float(torch.finfo(torch.bfloat16).max) < float(u) < float(torch.finfo(torch.float32).max)
+    check(y, *reference(c), kind)
+    rest = [r for r in range(9) if r != t]
+    assert torch.equal(y[rest], base[rest])
