@@ -453,7 +453,9 @@ NVFP4RS_API nvfp4_status nvfp4_group_wgrad_graphsafe(const nvfp4_matrix* dy, con
  * activation and the product in one launch.
  *   p = X_g W_g^T, W_g [2F, K]: rows 0..F-1 the gate, F..2F-1 the up projection
  *   h[t][f] = silu(p[t][f]) * p[t][F + f],  silu(v) = v / (1 + e^-v)
- * in fp32 from the unrounded p, rounded once to bf16.
+ * in fp32 from the unrounded p, rounded once to bf16. The exponential and the
+ * quotient are the hardware's: h is within (8 + |gate|) 2^-22 of itself before its
+ * rounding, at every gate; gates below -174 may give 0 for an h below 2^-116.
  *   x        HOST pointer to the operand [sum_M, K]
  *   w        HOST pointer to the operand [num_groups*2F, K]
  *   h        device bf16 [sum_M, F]

@@ -140,6 +140,18 @@ __device__ __forceinline__ uint64_t mul2x(uint64_t a, uint64_t b) {
   return d;
 }
 
+// e^(-|x|/2) (0 below 2^-126) and 1/x (x in [1, 2]) by the hardware's exponential and reciprocal
+__device__ __forceinline__ float half_exp(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fabsf(x) * -0.72134752f));  // -log2(e) / 2
+  return r;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // pairwise a*b + c, one rounding per element
 __device__ __forceinline__ uint64_t fma2x(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;

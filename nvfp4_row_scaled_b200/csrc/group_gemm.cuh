@@ -477,7 +477,17 @@ __device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float(static
 __device__ __forceinline__ float hi2(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
 __device__ __forceinline__ uint64_t pair2(uint32_t lo, uint32_t hi) { return static_cast<uint64_t>(hi) << 32 | lo; }
 __device__ __forceinline__ uint32_t bf16_pair(uint64_t v) { return bf16x2_rn(lo2(v), hi2(v)); }
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+// silu(g) u of a pair, g u / (1 + e^-g), as (g m / (1 + h^2)) (u m) with h = e^(-|g|/2) and m = 1 for
+// g >= 0, h below. The divisor is at most 2 (a fast quotient by e^-g is 0 from
+// 2^126 on), and h is a normal number down to g = -174.6, so that a large u still meets a
+// silu(g) far below 2^-126; below that the product, under 2^-116, is 0. Hardware exponential and
+// reciprocal: within a few parts in 2^23, plus |g| 2^-23 for the exponent's rounded argument.
+__device__ __forceinline__ uint64_t silu_times2(uint64_t g, uint64_t u) {
+  const float t0 = half_exp(lo2(g)), t1 = half_exp(hi2(g));
+  const uint64_t h = pack2(t0, t1), m = pack2(lo2(g) >= 0.0f ? 1.0f : t0, hi2(g) >= 0.0f ? 1.0f : t1);
+  const uint64_t d = fma2x(h, h, pack2(1.0f, 1.0f));
+  return mul2x(mul2x(mul2x(g, m), pack2(fast_rcp(lo2(d)), fast_rcp(hi2(d)))), mul2x(u, m));
+}
 
 // 32 rows x 32 features of a warp, lane = feature, y[i] = rows 2i and 2i + 1 as
 // bf16 pairs: turned in shared memory, stored as 16 bytes (8 features) a lane, so that
@@ -1205,7 +1215,7 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
               store_bf16(b, turn, p + a.ni, pitch, nc, features, lane);
             }
 #pragma unroll
-            for (int k = 0; k < 16; k++) b[k] = bf16x2_rn(silu(lo2(y[k])) * lo2(z[k]), silu(hi2(y[k])) * hi2(z[k]));
+            for (int k = 0; k < 16; k++) b[k] = bf16_pair(silu_times2(y[k], z[k]));
             store_bf16(b, turn, static_cast<uint16_t*>(a.out) + row * a.ni + t.i0 + 32 * q, a.ni, nc, features, lane);
           } else {
             if (kMode == kGemmAdapter) {

@@ -351,3 +351,30 @@ def test_large_gated_and_wgrad_pairs():
     run_gated(m, K, F, COMPACT, True)
     run_wgrad([304, 0, 512, 16], 1552, 1296, torch.bfloat16, COMPACT, COMPACT)
     run_wgrad([256, 0, 512], 1536, 1280, torch.float32, TILED, TILED)
+
+
+def test_gated_at_every_gate():
+    """Gates from -1400 to 1400, those among them at which e^-g is above 2^126 or
+    infinite and e^g below 2^-126, with up projections large enough that the product is an ordinary number:
+    h is held to the bound of gated_reference and half a step, with no absolute allowance."""
+    K, F, rows = 16, 64, 48
+    x, _ = random_matrix(rows, K, 28)
+    w, _ = random_matrix(2 * F, K, 29)
+    x["data"].fill_(0x22)  # 1.0
+    x["scale"].fill_(0x38)  # 1.0
+    x["s2"].fill_(2.0 ** -4)
+    w["data"].fill_(0x22)
+    w["scale"].fill_(0x38)
+    gate = torch.cat([torch.tensor([-1400.0, -300.0, -170.0, -104.0, -103.0, -90.0, -88.5, -88.0, -87.5, -87.0, -86.0, -30.0, -1.0,
+                                    -0.0, 1e-30, 0.5, 20.0, 87.0, 87.5, 88.5, 89.0, 104.0, 1400.0]),
+                      torch.linspace(-120, 120, F - 23)])
+    up = torch.cat([torch.full((12,), 2.0 ** 120), torch.ones(11), torch.full((F - 23,), 2.0 ** 60)])
+    w["s2"][:F], w["s2"][F:] = gate.cuda(), up.cuda()
+    h = torch.empty(rows, F, dtype=torch.bfloat16, device="cuda")
+    abi.nvfp4_group_gated_gemm(x, [rows], w, h)
+    p = torch.cat([gate, up]).double().expand(rows, -1)  # 16 ones, times 2^-4, times the factor: exact
+    want, lim = gated_reference(p, torch.zeros(rows, 2 * F, dtype=torch.float64), F)
+    got = h.double().cpu()
+    # the smallest normal bf16 is 2^-126; below it steps of 2^-133
+    err, room = (got - want).abs(), lim + 2.0 ** -8 * (want.abs() + lim) + 2.0 ** -134
+    assert bool((err <= room).all()), (gate[(err > room)[0]], got[0][(err > room)[0]], want[0][(err > room)[0]])
