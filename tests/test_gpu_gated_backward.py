@@ -137,3 +137,26 @@ def test_graphsafe_equals_host_split_and_replays():
     g.replay()
     torch.cuda.synchronize()
     assert int(st.item()) == abi.NVFP4_ERR_UNSUPPORTED and bool((d == 7.0).all())
+
+
+def test_every_gate():
+    """Gates at which e^-g is above 2^126 or infinite and e^g below 2^-126, dh and up large
+    and small: both gradients to the formula's bound and half a step, with no absolute allowance but
+    bf16's smallest steps."""
+    gate = torch.cat([torch.tensor([-1400.0, -300.0, -172.0, -150.0, -104.0, -103.0, -90.0, -88.5, -88.0, -87.5, -87.0, -30.0, -1.0,
+                                    -0.0, 1e-30, 0.5, 20.0, 87.0, 87.5, 88.5, 89.0, 104.0, 1400.0, 3e38]),
+                      torch.linspace(-172, 172, 104)])
+    up = torch.tensor([2.0 ** 100, 1.0, 2.0 ** 40, 2.0 ** -40])
+    dh0 = torch.tensor([2.0 ** 20, 1.0, 2.0 ** 80, 2.0 ** 30])
+    rows, F = 16, gate.numel()
+    gu = torch.cat([gate.expand(rows, F), up.repeat(4)[:, None].expand(rows, F)], 1).to(torch.bfloat16).contiguous().cuda()
+    dh = dh0.repeat(4)[:, None].expand(rows, F).to(torch.bfloat16).contiguous().cuda()
+    dh[:, 23] = 2.0 ** -10  # beside the gate of 3e38: products that fit
+    gu[:, F + 23] = 2.0 ** -10
+    d = torch.empty_like(gu)
+    abi.nvfp4_group_gated_backward(dh, gu, [rows], d)
+    want, lim = reference(dh, gu)
+    got = d.double().cpu()
+    err, room = (got - want).abs(), lim + 2.0 ** -8 * (want.abs() + lim) + 2.0 ** -134
+    bad = ~(err <= room)
+    assert not bool(bad.any()), (gu.cpu()[:, :F].repeat(1, 2)[bad], got[bad], want[bad])
