@@ -14,7 +14,8 @@
 //
 // Work split. A token block of 16 kMT rows; its K is split over the 8 warps of a
 // CTA and the `cn` CTAs of a cluster, the partial sums added in a fixed order
-// (warps, then cluster ranks), so the result does not depend on timing. The block's
+// (warps, then cluster ranks). cn is a function of K alone, so a token's result depends neither
+// on timing nor on the rows and adapters of the call. The block's
 // distinct adapters are dealt to `slots` CTAs: each multiplies the whole block by
 // its adapters and keeps the rows that use them. A decode step (a different
 // adapter on every row) runs its adapters side by side; a prompt has one

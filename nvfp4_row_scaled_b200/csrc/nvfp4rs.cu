@@ -872,10 +872,14 @@ template <int kMT, int kNT>
 nvfp4_status launch_shrink(const ShrinkArgs& s, int sms, cudaStream_t stream) {
   constexpr int kTok = 16 * kMT;
   const int64_t blocks = (s.rows + kTok - 1) / kTok;
-  // adapters side by side and K over a cluster while that fills the GPU
-  int slots = 1, cn = 1;
+  // adapters side by side while that fills the GPU
+  int slots = 1;
   while (slots < kTok && slots < s.adapters && blocks * slots < sms) slots *= 2;
-  while (cn < 8 && blocks * slots * cn <= (kMT == 1 ? sms : 2 * sms) && (s.K + 31) / 32 >= 16 * cn) cn *= 2;
+  // K over a pair of CTAs where each of their 16 warps gets a step of 32. By K alone: the order
+  // of a token's sum must not depend on the call's rows or adapters. us a call with 1, 2, 4, 8 CTAs:
+  // 64 rows of 4096, 64 adapters: 22.4, 22.3, 22.6, 24.9; 64 of 7168, rank 64: 28.8, 24.7, 22.7, 22.7;
+  // 2048 of 7168: 49.9, 48.1, 52.4, 62.8; 8192 of 7168: 167, 159, 168, 205; 8192 of 1024: 47, 50, 58, 58
+  const int cn = (s.K + 31) / 32 >= 16 ? 2 : 1;
   auto kernel = adapter_shrink_kernel<kMT, kNT>;
   const size_t smem = static_cast<size_t>(8) * kTok * 8 * kNT * 4;
   if (smem > 46 * 1024 &&

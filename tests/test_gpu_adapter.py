@@ -252,3 +252,26 @@ def test_u_above_the_largest_bf16(kind, dtype):
     check(y, *reference(c), kind)
     rest = [r for r in range(9) if r != t]
     assert torch.equal(y[rest], base[rest])
+
+
+def part_of(c, lo, hi):
+    return dict(c, xb=c["xb"][lo:hi].clone(), ids=c["ids"][lo:hi].clone(),
+                x=abi.matrix(*(c["x"][k][lo:hi].clone() for k in ("data", "scale", "s2"))))
+
+
+@pytest.mark.parametrize("K", [1024, 4096, 7168])
+def test_token_does_not_depend_on_the_size_of_the_call(K):
+    """The same bits among 4741 rows, 70, 17 and alone, with 8 adapters or 33 loaded: the first half's
+    sum over K has one order, however many CTAs share it."""
+    rows = 148 * 32 + 5
+    c = case(rows, K, 96, 16, 8, spread(rows, 8, "mixed"), 12)
+    y, st = run(c, torch.float32)
+    assert st == 0
+    for lo, hi in ((0, 70), (3, 20), (13, 14), (4740, 4741)):
+        z, _ = run(part_of(c, lo, hi), torch.float32)
+        assert torch.equal(y[lo:hi], z), (lo, hi)
+    more = part_of(c, 0, 70)
+    for k in ("a", "b", "f"):
+        more[k] = torch.cat([c[k], c[k], c[k], c[k], c[k][:1]])
+    z, _ = run(more, torch.float32)
+    assert torch.equal(y[:70], z)
