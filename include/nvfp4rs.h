@@ -391,8 +391,7 @@ NVFP4RS_API nvfp4_status nvfp4_mx_dequantize(const uint8_t* data, const uint8_t*
  * weight rows up to 2^31 - 1024, K and N up to 2^30, and with NVFP4_SCALE_TILED_128X4 an operand whose matrices are
  * multiples of 128 rows and of 128 columns (so 128-row groups for x).
  * With row-major (compact) scales groups may have any number of rows, 0 and
- * 1 included; their block scales are read in aligned 4-byte words, so up to 3
- * bytes behind a matrix's last scale may be read (and are ignored). K % 32 == 0
+ * 1 included. K % 32 == 0
  * takes the faster load path. Buffers must not overlap
  * the output. Rows of an output at or beyond the routed total are not written.
  */

@@ -117,6 +117,7 @@ struct GemmArgs {
   int32_t ni;        // output columns: I rows of a group (gated: of each half)
   int32_t nj;        // wgrad: J rows of a group
   int32_t K;         // contraction (wgrad: the group's rows instead)
+  int32_t j_whole;   // J rows whose row-major scales lie in whole aligned words: all, or all but the last one to three
   int32_t jt, jt_log;       // J rows of a tile: a power of two, 16 to 256; its logarithm
   uint32_t it, it_magic;    // I tiles of a group; floor(2^32 / it), 2^32 - 1 for it = 1
   int32_t jbulk;     // nonzero: J scales by bulk copies (tiled, and J tiles of whole 128-row blocks)
@@ -429,11 +430,10 @@ __device__ __forceinline__ void load_codes(uint32_t dst, const uint8_t* data, in
 enum ScaleRead : int { kRead16 = 0, kReadWords = 1, kReadBytes = 2, kReadTiled = 3 };
 
 // `left`: scales from p to the row's end. What is read raw is put together by
-// scale_words() later, so that a read is not waited for here. Every word that is
-// read holds a byte of the matrix, which starts on 16 bytes; where it ends inside
-// an aligned word, up to 3 bytes behind it are read with that word (memory is
-// allocated in larger units) and masked out. A check of the end here spilled
-// the loader's registers and took a weight gradient from 108 to 251 us.
+// scale_words() later, so that a read is not waited for here. Every aligned word that is
+// read lies in the matrix: the rows that own a byte of a word that the matrix ends inside
+// (from row a.j_whole on) are read byte by byte, by patch_scales(). A check of the end in
+// each read took 5003 ragged rows of 4096 from 108 to 121 us.
 __device__ __forceinline__ void read_scales(const uint8_t* p, int how, int32_t left, uint32_t (&w)[5]) {
 #pragma unroll
   for (int k = 0; k < 5; k++) w[k] = 0u;
@@ -448,7 +448,7 @@ __device__ __forceinline__ void read_scales(const uint8_t* p, int how, int32_t l
     const int b = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 3);
 #pragma unroll
     for (int k = 0; k < 5; k++)
-      if (4 * k < left + b) w[k] = gload(reinterpret_cast<const uint32_t*>(p - b) + k);
+      if (4 * k < min(left, 16) + b) w[k] = gload(reinterpret_cast<const uint32_t*>(p - b) + k);
   } else {
     const int step = how == kReadTiled ? kGScaleTile / 4 : 1;
 #pragma unroll
@@ -471,6 +471,16 @@ __device__ __forceinline__ void store_scales(uint8_t* dst, int lane, const uint3
 #pragma unroll
   for (int k = 0; k < 4; k++)
     *reinterpret_cast<uint4*>(dst + k * kGScaleTile + lane * 16) = make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
+}
+
+// Rows j0 .. j1 - 1 of a tile's J scales, a byte a lane (`src`: the first one's scales of the
+// k block, `cols` to the next row's, `left` to the row's end), over the zeros that store_scales() put there.
+__device__ __forceinline__ void patch_scales(uint8_t* dst, const uint8_t* src, int32_t cols, int32_t left, int j0, int j1,
+                                             int lane) {
+  __syncwarp();
+  if (lane >= min(left, 16)) return;
+  for (int j = j0; j < j1; j++, src += cols)
+    dst[((j >> 7) * 4 + (lane >> 2)) * kGScaleTile + (j & 31) * 16 + ((j & 127) >> 5) * 4 + (lane & 3)] = gload(src + lane);
 }
 
 __device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
@@ -943,6 +953,10 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
         uint32_t w[3][4][5];
       };
       Rows r;
+      // of a tile's J rows, those that read() reads
+      auto whole_rows = [&](const GemmTile& t) {
+        return kMode == kGemmWgrad ? t.jv : min(t.jv, a.j_whole - static_cast<int32_t>(t.jrow));
+      };
       auto read = [&] {
         const GemmTile& t = at.t;
         const int32_t cols = t.kc / 16, first = at.kb * 16, left = cols - first;
@@ -960,6 +974,7 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
         }
         if (!a.jbulk) {
           const int64_t jb = kMode == kGemmWgrad ? t.goff * a.nj / 16 : (t.jrow - t.j0) * cols;  // the group's first row
+          const int jv = whole_rows(t);
 #pragma unroll
           for (int h = 0; h < (kGated ? 1 : 2); h++) {
             if (128 * h >= t.jv) break;
@@ -973,7 +988,7 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
                      (jr & 31) * 16 + ((jr & 127) >> 5) * 4;
               else
                 pe = a.j.scale + jb + static_cast<int64_t>(jr) * cols + first;
-              read_scales(j < t.jv ? pe : nullptr, a.j.tiled ? kReadTiled : how, left, r.w[kJ + h][e]);
+              read_scales(j < jv ? pe : nullptr, a.j.tiled ? kReadTiled : how, left, r.w[kJ + h][e]);
             }
           }
         }
@@ -1045,6 +1060,11 @@ group_gemm_kernel(const __grid_constant__ Routing routing, const __grid_constant
           if (!kGated && t.jv > 128) {
             words(2, j_row + 128, a.j.tiled);
             store_scales(sf + Stage::kISf + 4 * kGScaleTile, lane, r.w[2]);
+          }
+          const int jw = whole_rows(t);
+          if (jw < t.jv) {
+            const int32_t cols = t.kc / 16, j0 = max(jw, 0), first = at.kb * 16;
+            patch_scales(sf + Stage::kISf, a.j.scale + (t.jrow + j0) * cols + first, cols, cols - first, j0, t.jv, lane);
           }
         }
         if (!kTma) cp_async_wait<0>();

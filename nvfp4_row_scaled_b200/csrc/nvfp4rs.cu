@@ -703,6 +703,12 @@ nvfp4_status launch_gemm(const Routing& routing, GemmArgs a, int64_t rows, int64
   }
   if (tiles == 0) return NVFP4_OK;
   if (tiles > INT32_MAX) return NVFP4_ERR_UNSUPPORTED;
+  // only token rows of K % 64 != 0 can end inside a word: weights, and wgrad's matrices, have a multiple of 16 rows
+  a.j_whole = static_cast<int32_t>(j_rows);
+  if (!kWgrad && !a.j.tiled && a.K > 0) {
+    const int64_t cols = a.K / 16;
+    a.j_whole -= static_cast<int32_t>((j_rows * cols % 4 + cols - 1) / cols);
+  }
   a.jt_log = 0;
   while ((1 << a.jt_log) < a.jt) a.jt_log++;
   a.it = static_cast<uint32_t>(pair ? it2 : it1);
@@ -719,8 +725,8 @@ nvfp4_status launch_gemm(const Routing& routing, GemmArgs a, int64_t rows, int64
     NVFP4_SPANS(SpanList{}
                     .add(a.j.data, jb / 2, false)
                     .add(a.i.data, ib / 2, false)
-                    .add(a.i.scale, (ib / 16 + 3) & ~size_t{3}, false)  // whole aligned words
-                    .add(a.j.scale, (jb / 16 + 3) & ~size_t{3}, false)
+                    .add(a.i.scale, ib / 16, false)
+                    .add(a.j.scale, jb / 16, false)
                     .add(a.i.s2, 4 * static_cast<size_t>(i_rows), false)
                     .add(a.j.s2, 4 * static_cast<size_t>(j_rows), false)
                     .routing(routing)

@@ -378,3 +378,28 @@ def test_gated_at_every_gate():
     # the smallest normal bf16 is 2^-126; below it steps of 2^-133
     err, room = (got - want).abs(), lim + 2.0 ** -8 * (want.abs() + lim) + 2.0 ** -134
     assert bool((err <= room).all()), (gate[(err > room)[0]], got[0][(err > room)[0]], want[0][(err > room)[0]])
+
+
+@pytest.mark.parametrize("m,K", [([1], 16), ([3], 48), ([129], 16), ([5, 0, 6], 80), ([2], 1040), ([131], 176), ([7], 1008),
+                                 ([66, 1], 272), ([257], 304)])
+def test_scales_that_end_inside_a_word(m, K):
+    """Row-major scales whose matrix ends 1, 2 or 3 bytes into an aligned word, NaN bytes behind
+    them: the values are right, and the bounds-checked build counts a read behind them."""
+    rows, E, N = sum(m), len(m), 48
+    assert rows * (K // 16) % 4
+    x, xv = random_matrix(rows, K, 30)
+    w, wv = random_matrix(E * 2 * N, K, 31)
+    n = x["scale"].numel()
+    buf = torch.full((n + 64,), 0x7F, dtype=torch.uint8, device="cuda")
+    buf[:n] = x["scale"].view(-1)
+    x["scale"] = buf[:n].view(rows, K // 16)
+    want, lim = stacked(m, xv, wv, 2 * N)
+    y = torch.empty(rows, 2 * N, device="cuda")
+    abi.nvfp4_group_gemm(x, m, w, y)
+    check(y, want, lim)
+    x["s2"] *= 2.0 ** -8
+    h, p = torch.empty(rows, N, dtype=torch.bfloat16, device="cuda"), torch.empty(rows, 2 * N, dtype=torch.bfloat16, device="cuda")
+    abi.nvfp4_group_gated_gemm(x, m, w, h, gate_up=p)
+    want, lim = stacked(m, xv * 2.0 ** -8, wv, 2 * N)
+    check(p, want, lim)
+    check(h, *gated_reference(want, lim, N))
