@@ -831,7 +831,7 @@ nvfp4_status launch_gated_backward(const Routing& routing, const void* dh, const
   const int64_t per = (chunks + cn - 1) / cn;
   if (per > 32) return NVFP4_ERR_UNSUPPORTED;
   const size_t smem = static_cast<size_t>(per) * 2 * kBwChunk * 4 + sizeof(int32_t) * (routing.E + 1);
-  auto kernel = gated_backward_kernel<Routing>;
+  auto kernel = out == gate_up ? gated_backward_kernel<Routing, true> : gated_backward_kernel<Routing, false>;
   if (smem > 46 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
     return NVFP4_ERR_CUDA;

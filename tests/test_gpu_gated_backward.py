@@ -160,3 +160,25 @@ def test_every_gate():
     err, room = (got - want).abs(), lim + 2.0 ** -8 * (want.abs() + lim) + 2.0 ** -134
     bad = ~(err <= room)
     assert not bool(bad.any()), (gu.cpu()[:, :F].repeat(1, 2)[bad], got[bad], want[bad])
+
+
+@pytest.mark.parametrize("m,F", [([16], 16), ([48, 80], 8192), ([16, 0, 48, 32], 272), ([32], 65536), ([16] * 37, 2048),
+                                 ([4096, 16, 2064], 1024)])
+def test_in_place(m, F):
+    """d_gate_up written over gate_up: the same bits as beside it, over clusters of 1 to 8 CTAs
+    and tiles that hold several groups, host-split and graph-safe."""
+    rows, E = sum(m), len(m)
+    dh, gu = inputs(rows, F, 6)
+    d, (ra, ca) = torch.empty_like(gu), abi.alloc_amax(rows, 2 * F, E)
+    abi.nvfp4_group_gated_backward(dh, gu, m, d, ra, ca)
+    fd, offs = abi.routing_tensors(m, 2 * F)
+    st = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    for graphsafe in (False, True):
+        p = gu.clone()
+        ra2, ca2 = abi.alloc_amax(rows, 2 * F, E)
+        if graphsafe:
+            abi.nvfp4_group_gated_backward_graphsafe(dh, p, fd, offs, p, st, ra2, ca2)
+            assert int(st.item()) == 0
+        else:
+            abi.nvfp4_group_gated_backward(dh, p, m, p, ra2, ca2)
+        assert torch.equal(p, d) and torch.equal(ra2, ra) and torch.equal(ca2, ca)
