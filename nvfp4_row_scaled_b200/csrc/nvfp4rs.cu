@@ -43,6 +43,15 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 nvfp4_status cuda_status(cudaError_t e) { return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA; }
 
+// Lets a kernel launch with up to `bytes` of dynamic shared memory. The limit belongs to the function, not
+// to the launch: always set to the most any call of the kernel takes, so that calls of several
+// host threads write the same value (with each call's own size one could lower
+// it between another's setting and its launch).
+template <class Kernel>
+bool allow_smem(Kernel kernel, size_t bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) == cudaSuccess;
+}
+
 #ifdef NVFP4_CHECK_BOUNDS
 // The checked debug build: the byte ranges a launch may touch, registered on
 // its stream just before it (see bounds.cuh). The first range must be an
@@ -255,11 +264,8 @@ nvfp4_status launch_amax(const Routing& routing, const void* x, int64_t rows, in
   const int cn = amax_cluster(K, tiles, sms);
   const size_t smem = static_cast<size_t>(amax_cta_cols(K, cn)) * sizeof(uint32_t) + sizeof(int32_t) * (E + 1);
   auto kernel = group_amax_kernel<Routing>;
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
-    if (e != cudaSuccess) return NVFP4_ERR_CUDA;
-  }
+  constexpr size_t kMost = sizeof(uint32_t) * kMaxAmaxCols + sizeof(int32_t) * (NVFP4_MAX_GROUPS + 1);
+  if (smem > 46 * 1024 && !allow_smem(kernel, kMost)) return NVFP4_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * cn));
   cfg.blockDim = dim3(kAmaxThreads);
@@ -300,9 +306,7 @@ nvfp4_status launch_cast(const Routing& routing, const void* x, int64_t rows, in
   const int64_t units = (tiles + kPGroups - 1) / kPGroups;
   static_assert(plain_smem_bytes(NVFP4_MAX_GROUPS) + 1024 <= 227 * 1024, "cast kernel shared memory");
   const size_t smem = plain_smem_bytes(E) + 1024;  // + room to align the block to 1024 bytes
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e != cudaSuccess) return NVFP4_ERR_CUDA;
+  if (!allow_smem(kernel, plain_smem_bytes(NVFP4_MAX_GROUPS) + 1024)) return NVFP4_ERR_CUDA;
   int dev = 0, sms = 0, per_sm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
@@ -357,9 +361,7 @@ nvfp4_status launch_quantize(const Routing& routing, const void* x, int64_t rows
   auto kernel = out->scale_layout == NVFP4_SCALE_TILED_128X4 ? group_quantize_kernel<Routing, true>
                                                              : group_quantize_kernel<Routing, false>;
   const size_t smem = quantize_smem_bytes(E) + 1024;  // + room to align the block to 1024 bytes
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e != cudaSuccess) return NVFP4_ERR_CUDA;
+  if (!allow_smem(kernel, quantize_smem_bytes(NVFP4_MAX_GROUPS) + 1024)) return NVFP4_ERR_CUDA;
   int dev = 0, sms = 0, per_sm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
@@ -503,9 +505,7 @@ nvfp4_status launch_mx_cast(const Routing& routing, const void* x, int64_t rows,
   if (!x_tensor_map(&map, x, rows, K)) return NVFP4_ERR_CUDA;
   auto kernel = mx_cast_kernel<Routing>;
   const size_t smem = mx_smem_bytes(E) + 1024;  // + room to align the block to 1024 bytes
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-      cudaSuccess)
-    return NVFP4_ERR_CUDA;
+  if (!allow_smem(kernel, mx_smem_bytes(NVFP4_MAX_GROUPS) + 1024)) return NVFP4_ERR_CUDA;
   int dev = 0, sms = 0, per_sm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
@@ -651,9 +651,9 @@ nvfp4_status start_gemm(const Routing& routing, const GemmArgs& a, int64_t i_row
   auto kernel = group_gemm_kernel<Routing, kMode, kTma, kPair>;
   constexpr bool kGated = kMode == kGemmGated;
   const size_t smem = gemm_smem_bytes<kGated>(routing.E) + 1024;  // + room to align the block to 1024 bytes
-  static_assert(gemm_smem_bytes<kGated>(NVFP4_MAX_GROUPS) + 1024 <= 227 * 1024, "product kernel shared memory");
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-    return NVFP4_ERR_CUDA;
+  constexpr size_t kMost = gemm_smem_bytes<kGated>(NVFP4_MAX_GROUPS) + 1024;
+  static_assert(kMost <= 227 * 1024, "product kernel shared memory");
+  if (!allow_smem(kernel, kMost)) return NVFP4_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   const int64_t grid = kPair ? 2 * std::min<int64_t>(tiles, sms / 2) : std::min<int64_t>(tiles, sms);
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -832,9 +832,8 @@ nvfp4_status launch_gated_backward(const Routing& routing, const void* dh, const
   if (per > 32) return NVFP4_ERR_UNSUPPORTED;
   const size_t smem = static_cast<size_t>(per) * 2 * kBwChunk * 4 + sizeof(int32_t) * (routing.E + 1);
   auto kernel = out == gate_up ? gated_backward_kernel<Routing, true> : gated_backward_kernel<Routing, false>;
-  if (smem > 46 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-    return NVFP4_ERR_CUDA;
+  constexpr size_t kMost = size_t{32} * 2 * kBwChunk * 4 + sizeof(int32_t) * (NVFP4_MAX_GROUPS + 1);
+  if (smem > 46 * 1024 && !allow_smem(kernel, kMost)) return NVFP4_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * cn));
   cfg.blockDim = dim3(kBwThreads);
@@ -887,10 +886,8 @@ nvfp4_status launch_shrink(const ShrinkArgs& s, int sms, cudaStream_t stream) {
   // 2048 of 7168: 49.9, 48.1, 52.4, 62.8; 8192 of 7168: 167, 159, 168, 205; 8192 of 1024: 47, 50, 58, 58
   const int cn = (s.K + 31) / 32 >= 16 ? 2 : 1;
   auto kernel = adapter_shrink_kernel<kMT, kNT>;
-  const size_t smem = static_cast<size_t>(8) * kTok * 8 * kNT * 4;
-  if (smem > 46 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-    return NVFP4_ERR_CUDA;
+  constexpr size_t smem = static_cast<size_t>(8) * kTok * 8 * kNT * 4;
+  if (smem > 46 * 1024 && !allow_smem(kernel, smem)) return NVFP4_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks * cn), static_cast<unsigned>(slots));
   cfg.blockDim = dim3(kAdThreads);
