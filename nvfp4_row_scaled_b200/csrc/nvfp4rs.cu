@@ -46,7 +46,9 @@ nvfp4_status cuda_status(cudaError_t e) { return e == cudaSuccess ? NVFP4_OK : N
 // Lets a kernel launch with up to `bytes` of dynamic shared memory. The limit belongs to the function, not
 // to the launch: always set to the most any call of the kernel takes, so that calls of several
 // host threads write the same value (with each call's own size one could lower
-// it between another's setting and its launch).
+// it between another's setting and its launch). It also makes the device's context current in
+// a host thread that has made no CUDA call yet, without which cuTensorMapEncodeTiled
+// fails: every call does it before it encodes a map.
 template <class Kernel>
 bool allow_smem(Kernel kernel, size_t bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) == cudaSuccess;
@@ -297,8 +299,6 @@ nvfp4_status launch_cast(const Routing& routing, const void* x, int64_t rows, in
   const int64_t tiles = ((rows + kRows - 1) / kRows) * ((K + kCols - 1) / kCols);
   const bool s2_work = do_col && E > 0 && K > 0;
   if (tiles == 0 && !s2_work) return NVFP4_OK;
-  CUtensorMap map;
-  if (!x_tensor_map(&map, x, rows, K)) return NVFP4_ERR_CUDA;
   // tiled scales come with 128-row groups and K % 128 == 0 only (checked on
   // the host, or on the device by the routing): every tile is plain
   const bool tiled = out->scale_layout == NVFP4_SCALE_TILED_128X4;
@@ -307,6 +307,8 @@ nvfp4_status launch_cast(const Routing& routing, const void* x, int64_t rows, in
   static_assert(plain_smem_bytes(NVFP4_MAX_GROUPS) + 1024 <= 227 * 1024, "cast kernel shared memory");
   const size_t smem = plain_smem_bytes(E) + 1024;  // + room to align the block to 1024 bytes
   if (!allow_smem(kernel, plain_smem_bytes(NVFP4_MAX_GROUPS) + 1024)) return NVFP4_ERR_CUDA;
+  CUtensorMap map;
+  if (!x_tensor_map(&map, x, rows, K)) return NVFP4_ERR_CUDA;
   int dev = 0, sms = 0, per_sm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
@@ -356,12 +358,12 @@ nvfp4_status launch_quantize(const Routing& routing, const void* x, int64_t rows
   const int64_t tiles = (rows / kRows) * (K / kCols);
   const bool s2_work = do_col && E > 0 && K > 0;
   if (tiles == 0 && !s2_work) return NVFP4_OK;
-  CUtensorMap map;
-  if (!x_tensor_map(&map, x, rows, K)) return NVFP4_ERR_CUDA;
   auto kernel = out->scale_layout == NVFP4_SCALE_TILED_128X4 ? group_quantize_kernel<Routing, true>
                                                              : group_quantize_kernel<Routing, false>;
   const size_t smem = quantize_smem_bytes(E) + 1024;  // + room to align the block to 1024 bytes
   if (!allow_smem(kernel, quantize_smem_bytes(NVFP4_MAX_GROUPS) + 1024)) return NVFP4_ERR_CUDA;
+  CUtensorMap map;
+  if (!x_tensor_map(&map, x, rows, K)) return NVFP4_ERR_CUDA;
   int dev = 0, sms = 0, per_sm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
@@ -501,11 +503,11 @@ nvfp4_status launch_mx_cast(const Routing& routing, const void* x, int64_t rows,
                             const nvfp4_mx_outputs* out, cudaStream_t stream) {
   const int64_t tiles = ((rows + kRows - 1) / kRows) * ((K + kCols - 1) / kCols);
   if (tiles == 0) return NVFP4_OK;
-  CUtensorMap map;
-  if (!x_tensor_map(&map, x, rows, K)) return NVFP4_ERR_CUDA;
   auto kernel = mx_cast_kernel<Routing>;
   const size_t smem = mx_smem_bytes(E) + 1024;  // + room to align the block to 1024 bytes
   if (!allow_smem(kernel, mx_smem_bytes(NVFP4_MAX_GROUPS) + 1024)) return NVFP4_ERR_CUDA;
+  CUtensorMap map;
+  if (!x_tensor_map(&map, x, rows, K)) return NVFP4_ERR_CUDA;
   int dev = 0, sms = 0, per_sm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
@@ -638,6 +640,12 @@ int64_t product_tiles(const DeviceRouting& r, int64_t rows, int64_t nj, int64_t 
 template <int kMode, bool kTma, bool kPair, class Routing>
 nvfp4_status start_gemm(const Routing& routing, const GemmArgs& a, int64_t i_rows, int64_t j_rows, int64_t tiles, int sms,
                         cudaStream_t stream) {
+  auto kernel = group_gemm_kernel<Routing, kMode, kTma, kPair>;
+  constexpr bool kGated = kMode == kGemmGated;
+  const size_t smem = gemm_smem_bytes<kGated>(routing.E) + 1024;  // + room to align the block to 1024 bytes
+  constexpr size_t kMost = gemm_smem_bytes<kGated>(NVFP4_MAX_GROUPS) + 1024;
+  static_assert(kMost <= 227 * 1024, "product kernel shared memory");
+  if (!allow_smem(kernel, kMost)) return NVFP4_ERR_CUDA;
   CUtensorMap imap, jmap, jmap_small;
   if (kTma) {
     if (!code_tensor_map(&imap, a.i.data, i_rows, a.K, kGI) || !code_tensor_map(&jmap, a.j.data, j_rows, a.K, kGBigJ) ||
@@ -648,12 +656,6 @@ nvfp4_status start_gemm(const Routing& routing, const GemmArgs& a, int64_t i_row
     std::memset(&jmap, 0, sizeof(jmap));
     std::memset(&jmap_small, 0, sizeof(jmap_small));
   }
-  auto kernel = group_gemm_kernel<Routing, kMode, kTma, kPair>;
-  constexpr bool kGated = kMode == kGemmGated;
-  const size_t smem = gemm_smem_bytes<kGated>(routing.E) + 1024;  // + room to align the block to 1024 bytes
-  constexpr size_t kMost = gemm_smem_bytes<kGated>(NVFP4_MAX_GROUPS) + 1024;
-  static_assert(kMost <= 227 * 1024, "product kernel shared memory");
-  if (!allow_smem(kernel, kMost)) return NVFP4_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   const int64_t grid = kPair ? 2 * std::min<int64_t>(tiles, sms / 2) : std::min<int64_t>(tiles, sms);
   cfg.gridDim = dim3(static_cast<unsigned>(grid));

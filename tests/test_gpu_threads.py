@@ -113,3 +113,58 @@ def test_two_threads_with_calls_of_different_sizes(what):
     for (_, outs), w in zip(calls, want):
         for a, b in zip(outs, w):
             assert torch.equal(a, b)
+
+
+def cast_only(m, K, seed):
+    call, outs = cast(m, K, seed)
+    call(None)
+    x = torch.randn(sum(m), K, generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16).cuda()
+    ra, ca = outs[:2]
+    out = abi.alloc_outputs(sum(m), K, len(m))
+    return lambda s: abi.nvfp4_group_cast(x, m, ra, ca, out, stream=s), list(out.values())
+
+
+def wgrad(m, seed):
+    q = [random_matrix(32, sum(m), seed + i)[0] for i in range(2)]
+    dw = torch.empty(1, 32, 32, device="cuda")
+    return lambda s: abi.nvfp4_group_wgrad(*q, m, dw, stream=s), [dw]
+
+
+def gemm_odd(seed):
+    x, _ = random_matrix(5, 48, seed)
+    w, _ = random_matrix(16, 48, seed + 1)
+    y = torch.empty(5, 16, device="cuda")
+    return lambda s: abi.nvfp4_group_gemm(x, [5], w, y, stream=s), [y]
+
+
+FIRST = {
+    "gemm": lambda: gemm([7], 1), "gemm_without_maps": lambda: gemm_odd(2), "gated": lambda: gated([7], 3),
+    "wgrad": lambda: wgrad([64], 4), "gated_backward": lambda: backward([16], 64, 5), "cast": lambda: cast([16], 64, 6),
+    "cast_alone": lambda: cast_only([16], 64, 7), "mx_cast": lambda: cast([32], 64, 8, True), "quantize": lambda: quantize([128], 128, 9),
+}
+
+
+@pytest.mark.parametrize("what", sorted(FIRST))
+def test_first_cuda_call_of_a_thread(what):
+    """A call from a host thread that has made no CUDA call before."""
+    call, outs = FIRST[what]()
+    call(None)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in outs]
+    for t in outs:
+        t.view(torch.uint8).fill_(0xA5)
+    torch.cuda.synchronize()
+    stream, errors = torch.cuda.Stream(), []
+
+    def first():
+        try:
+            call(stream)
+        except Exception as e:  # noqa: BLE001 - reported by the test's thread
+            errors.append(e)
+    t = threading.Thread(target=first)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors[0]
+    for a, b in zip(outs, want):
+        assert torch.equal(a, b)
