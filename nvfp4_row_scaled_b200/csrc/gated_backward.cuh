@@ -172,8 +172,10 @@ gated_backward_kernel(const __grid_constant__ Routing routing, const uint4* __re
     }
   }
   __syncthreads();
+  // col_amax is zero; waited for by every CTA, those without rows too: what follows on the stream
+  // waits for this kernel and not for the zeroing before it
+  if (col_amax != nullptr) grid_dependency_wait();
   if (active && !mixed && col_amax != nullptr) {
-    grid_dependency_wait();  // col_amax is zero
     float* dst = col_amax + static_cast<size_t>(g_first) * 2 * F;
     for (int c = t; c < per * 2 * kBwChunk; c += kBwThreads) {
       const int col = ((c / (2 * kBwChunk)) * cn + rank) * kBwChunk + (c & (kBwChunk - 1));

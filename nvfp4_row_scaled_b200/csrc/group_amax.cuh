@@ -206,8 +206,10 @@ group_amax_kernel(const __grid_constant__ Routing routing, const uint4* __restri
     }
   }
   __syncthreads();
+  // col_amax is zero; waited for by every CTA, those without rows too: what follows on the stream
+  // waits for this kernel and not for the zeroing before it
+  if (col_amax != nullptr) grid_dependency_wait();
   if (active && !mixed && col_amax != nullptr) {
-    grid_dependency_wait();  // col_amax is zero
     float* dst = col_amax + static_cast<size_t>(g_first) * K;
     for (int c = t; c < cols; c += kAmaxThreads) {
       const int gc = (((c >> 7) * cn + rank) << 7) | (c & 127);

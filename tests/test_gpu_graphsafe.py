@@ -177,3 +177,25 @@ def test_config4_full_capacity_replays_match_host_split_and_oracle():
         assert_identical(got, gpu_cast(w.x, splits), keys=list(KEYS) + ["row_amax", "col_amax"],
                          what=f"full replay {i}")
         check_groups_against_oracle(got, xb, splits, w.K, what=f"full replay {i}")
+
+
+@pytest.mark.parametrize("what", ["amax", "gated_backward"])
+def test_column_amax_of_no_rows_is_zero_for_the_cast_behind_it(what):
+    """A routing that leaves every group empty: col_amax, full of sevens before the call, is zero for
+    the cast launched right behind it (col_s2 = 0 for an empty group)."""
+    E, K, cap = 256, 32768, 16
+    fd, offs = abi.routing_tensors([0] * E, K)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ra, ca = abi.alloc_amax(cap, K, E)
+    x = torch.zeros(cap, K, dtype=torch.bfloat16, device="cuda")
+    dh = torch.zeros(cap, K // 2, dtype=torch.bfloat16, device="cuda")
+    d = torch.zeros_like(x)
+    out = abi.alloc_outputs(cap, K, E)
+    for _ in range(30):
+        ca.fill_(7.0)
+        if what == "amax":
+            abi.nvfp4_group_amax_graphsafe(x, fd, offs, ra, ca, st)
+        else:
+            abi.nvfp4_group_gated_backward_graphsafe(dh, x, fd, offs, d, st, ra, ca)
+        abi.nvfp4_group_cast_graphsafe(x, fd, offs, ra, ca, out, st)
+        assert bool((out["col_s2"] == 0).all()) and bool((ca == 0).all())
