@@ -1174,7 +1174,7 @@ nvfp4_status nvfp4_group_gemm_graphsafe(const nvfp4_matrix* x, int64_t capacity_
                      routing);
   if (s != NVFP4_OK) return s;
   s = cuda_status(cudaMemsetAsync(status_dev, 0, sizeof(int32_t), stream));
-  if (s != NVFP4_OK || capacity_rows == 0 || N == 0) return s;
+  if (s != NVFP4_OK || capacity_rows == 0 || N == 0 || num_groups == 0) return s;
   return launch_gemm<kGemmPlain>(routing, gemm_args(x, K, w, N, y, y_dtype == NVFP4_OUT_F32), capacity_rows,
                                  num_groups * N, capacity_rows, stream);
 }
@@ -1207,7 +1207,7 @@ nvfp4_status nvfp4_group_gated_gemm_graphsafe(const nvfp4_matrix* x, int64_t cap
                      routing);
   if (s != NVFP4_OK) return s;
   s = cuda_status(cudaMemsetAsync(status_dev, 0, sizeof(int32_t), stream));
-  if (s != NVFP4_OK || capacity_rows == 0 || F == 0) return s;
+  if (s != NVFP4_OK || capacity_rows == 0 || F == 0 || num_groups == 0) return s;
   GemmArgs a = gemm_args(x, K, w, F, h_bf16, false);
   a.pre = static_cast<uint16_t*>(gate_up_bf16);
   return launch_gemm<kGemmGated>(routing, a, capacity_rows, num_groups * 2 * F, capacity_rows, stream);

@@ -403,3 +403,18 @@ def test_scales_that_end_inside_a_word(m, K):
     want, lim = stacked(m, xv * 2.0 ** -8, wv, 2 * N)
     check(p, want, lim)
     check(h, *gated_reference(want, lim, N))
+
+
+def test_graphsafe_without_groups_writes_nothing():
+    """No groups, rows allocated: nothing is routed, so nothing is written, as in the casts."""
+    K, N, cap = 64, 32, 40
+    x, _ = random_matrix(cap, K, 32)
+    w, _ = random_matrix(0, K, 33)
+    fd, offs = torch.zeros(0, dtype=torch.int64, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda")
+    for arrays in ((fd, offs), (None, None)):
+        st = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+        y = torch.full((cap, N), 7.0, device="cuda")
+        abi.nvfp4_group_gemm_graphsafe(x, *arrays, w, y, st, num_groups=0)
+        h = torch.full((cap, N), 7.0, dtype=torch.bfloat16, device="cuda")
+        abi.nvfp4_group_gated_gemm_graphsafe(x, *arrays, w, h, st, num_groups=0)
+        assert int(st.item()) == 0 and bool((y == 7.0).all()) and bool((h == 7.0).all())
