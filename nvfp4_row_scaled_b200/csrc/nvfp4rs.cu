@@ -149,8 +149,8 @@ nvfp4_status host_routing(const int64_t* m_splits, int32_t E, int64_t sum_M, Hos
   for (int32_t g = 0; g < E; g++) {
     if (m_splits[g] < 0) return NVFP4_ERR_INVALID_ARG;
     if (m_splits[g] % align != 0) unaligned = true;
+    if (m_splits[g] > sum_M - total) return NVFP4_ERR_INVALID_ARG;  // before the sum, which could overflow
     total += m_splits[g];
-    if (total > sum_M) return NVFP4_ERR_INVALID_ARG;
     r.off[g + 1] = static_cast<int32_t>(total);
   }
   if (total != sum_M) return NVFP4_ERR_INVALID_ARG;

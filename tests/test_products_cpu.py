@@ -136,3 +136,18 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes(L):
         abi._width(w, x, 3)
     with pytest.raises(ValueError, match="float32 or bfloat16"):
         abi._out_dtype(torch.zeros(1, dtype=torch.float16), "y")
+
+
+@pytest.mark.parametrize("m", [[64, (1 << 63) - 1, (1 << 63) - 1, 2], [64, (1 << 63) - 16, (1 << 63) - 16, 32], [16, (1 << 63) - 16, 64]])
+def test_splits_whose_sum_overflows(L, m):
+    """Sizes that add up to 64 only modulo 2^64 are refused by every host-split call."""
+    out = abi.Outputs(row_data=FAKE, row_scale=FAKE, row_s2=FAKE)
+    mx = abi.MxOutputs(row_data=FAKE, row_scale=FAKE)
+    n, ap = len(m), splits(m)
+    assert L.nvfp4_group_gemm(mat(), 64, 128, ap, n, mat(), 32, FAKE, BF16, None) == BAD
+    assert L.nvfp4_group_gated_gemm(mat(), 64, 128, ap, n, mat(), 32, FAKE, FAKE, None) == BAD
+    assert L.nvfp4_group_wgrad(mat(), mat(), 64, ap, n, 32, 48, FAKE, F32, None) == BAD
+    assert L.nvfp4_group_gated_backward(FAKE, FAKE, 64, 32, ap, n, FAKE, FAKE, FAKE, None) == BAD
+    assert L.nvfp4_group_amax(FAKE, 64, 128, ap, n, FAKE, FAKE, None) == BAD
+    assert L.nvfp4_group_cast(FAKE, 64, 128, ap, n, FAKE, FAKE, ctypes.byref(out), None) == BAD
+    assert L.nvfp4_mx_group_cast(FAKE, 64, 128, ap, n, ctypes.byref(mx), None) == BAD
