@@ -391,9 +391,12 @@ NVFP4RS_API nvfp4_status nvfp4_mx_dequantize(const uint8_t* data, const uint8_t*
  * weight rows up to 2^31 - 1024, K and N up to 2^30, and with NVFP4_SCALE_TILED_128X4 an operand whose matrices are
  * multiples of 128 rows and of 128 columns (so 128-row groups for x).
  * With row-major (compact) scales groups may have any number of rows, 0 and
- * 1 included. K % 32 == 0
- * takes the faster load path. Buffers must not overlap
- * the output. Rows of an output at or beyond the routed total are not written.
+ * 1 included. K % 32 == 0 takes the faster load path. Buffers must not overlap the
+ * output. Rows of an output at or beyond the routed total are not written.
+ * Every wait inside the kernels is bounded (seconds); a kernel that gave one up, which
+ * is not expected, leaves its output incomplete. The calls with a status word report
+ * it there (NVFP4_ERR_TIMEOUT); the host-split products, whose call has returned by
+ * then, cannot.
  */
 typedef struct {
   const uint8_t* data;  /* device, codes */
@@ -512,8 +515,13 @@ NVFP4RS_API size_t nvfp4_adapter_workspace_bytes(int64_t rows, int32_t rank);
  *   y[t] = X[t] W^T + factor[a] (x[t] A_a^T) B_a^T,   a = ids[t]; no second
  *   term where ids[t] == -1
  * X, W the NVFP4 operands [rows, K] and [N, K] (x_bf16's rowwise cast and the
- * shared weights), x, A, B bf16. u = factor (x A^T) is kept in fp32, its second
- * product added in fp32 to the projection before the one rounding of y.
+ * shared weights), x, A, B bf16. u = factor (x A^T) is summed and kept in fp32. Its
+ * product with B takes bf16 terms of u whose sum is within 2^-25 of it for an
+ * fp32 y and within 2^-17 for a bf16 y (whose own rounding is 2^-8: the difference
+ * shows only where the adapter cancels the projection); it is summed in fp32 and added
+ * in fp32 to the projection before the one rounding of y. Infinities and NaN in A,
+ * B, factor and u give what the formula gives, in the tokens that use them and no
+ * others.
  *   x_bf16   device bf16 [rows, K]
  *   a_bf16   device bf16 [num_adapters, rank, K]
  *   b_bf16   device bf16 [num_adapters, N, rank]
@@ -527,7 +535,8 @@ NVFP4RS_API size_t nvfp4_adapter_workspace_bytes(int64_t rows, int32_t rank);
  *            [-1, num_adapters) (that token gets no adapter)
  * rank a multiple of 8 (else NVFP4_ERR_INVALID_ARG) up to 64 (else
  * NVFP4_ERR_UNSUPPORTED). A token's result does not depend on the adapters of
- * the other tokens. A memset of status and two launches.
+ * the other tokens, nor on the call's rows and adapters. A memset of status and two
+ * launches.
  */
 NVFP4RS_API nvfp4_status nvfp4_adapter_gemm(const void* x_bf16, const nvfp4_matrix* x, int64_t rows, int64_t K,
                                 const nvfp4_matrix* w, int64_t N, const void* a_bf16, const void* b_bf16,

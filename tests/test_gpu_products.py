@@ -418,3 +418,69 @@ def test_graphsafe_without_groups_writes_nothing():
         h = torch.full((cap, N), 7.0, dtype=torch.bfloat16, device="cuda")
         abi.nvfp4_group_gated_gemm_graphsafe(x, *arrays, w, h, st, num_groups=0)
         assert int(st.item()) == 0 and bool((y == 7.0).all()) and bool((h == 7.0).all())
+
+
+def test_longest_contraction():
+    """The longest K: a tile's products take a second, and the warps that wait for them wait that
+    long. Ones at both ends, zeros between."""
+    K, N = 1 << 30, 16
+    x = abi.matrix(torch.zeros(1, K // 2, dtype=torch.uint8, device="cuda"), torch.full((1, K // 16), 0x38, dtype=torch.uint8, device="cuda"),
+                   torch.ones(1, device="cuda"))
+    w = abi.matrix(torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda"), torch.full((N, K // 16), 0x38, dtype=torch.uint8, device="cuda"),
+                   torch.arange(1.0, N + 1, device="cuda"))
+    for t in (x["data"], w["data"]):
+        t[:, :100] = 0x22
+        t[:, -60:] = 0x22
+    y = torch.full((1, N), 7.0, device="cuda")
+    abi.nvfp4_group_gemm(x, [1], w, y)
+    assert torch.equal(y.cpu(), 320.0 * torch.arange(1.0, N + 1)[None])
+
+
+def test_1024_groups():
+    """As many groups as a call takes, most of them empty or of one row, host-split and graph-safe."""
+    E, K, N = 1024, 64, 32
+    m = [(0, 1, 0, 3)[g % 4] for g in range(E)]
+    m[500], m[-1] = 140, 33
+    rows = sum(m)
+    x, xv = random_matrix(rows, K, 34)
+    w, wv = random_matrix(E * N, K, 35)
+    buf, y = guarded(rows, N, torch.float32)
+    abi.nvfp4_group_gemm(x, m, w, y)
+    check(y, *stacked(m, xv, wv, N))
+    assert bool((buf[rows:] == 7.0).all())
+    fd, offs, st = routings(m, K, rows)
+    z = torch.empty_like(y)
+    abi.nvfp4_group_gemm_graphsafe(x, fd, offs, w, z, st)
+    assert int(st.item()) == 0 and torch.equal(y, z)
+    run_wgrad([0, 16, 0, 0] * 255 + [48, 0, 16, 0], 32, 16, torch.float32, COMPACT, COMPACT)
+
+
+def test_gated_rows_do_not_depend_on_the_size_of_the_call():
+    """The same bits from a call large enough for pairs of CTAs, from a few rows and from one."""
+    K, F, rows = 1056, 1040, 4100
+    x, _ = random_matrix(rows, K, 36)
+    x["s2"] *= 2.0 ** -8
+    w, _ = random_matrix(2 * F, K, 37)
+    h, p = torch.empty(rows, F, dtype=torch.bfloat16, device="cuda"), torch.empty(rows, 2 * F, dtype=torch.bfloat16, device="cuda")
+    abi.nvfp4_group_gated_gemm(x, [rows], w, h, gate_up=p)
+    for lo, hi in ((0, 1), (7, 60), (4000, 4100)):
+        part = abi.matrix(*(x[k][lo:hi].clone() for k in ("data", "scale", "s2")))
+        h2, p2 = torch.empty_like(h[lo:hi]), torch.empty_like(p[lo:hi])
+        abi.nvfp4_group_gated_gemm(part, [hi - lo], w, h2, gate_up=p2)
+        assert torch.equal(h2, h[lo:hi]) and torch.equal(p2, p[lo:hi]), (lo, hi)
+
+
+def test_weight_gradient_does_not_depend_on_the_other_groups():
+    """A group's gradient among 40 groups (pairs of CTAs) and alone: the same bits."""
+    m, N, K = [48 + 16 * (g % 5) for g in range(40)], 528, 784
+    dy, _ = random_columns(m, N, 500, COMPACT)
+    x, _ = random_columns(m, K, 600, COMPACT)
+    dw = torch.empty(40, N, K, device="cuda")
+    abi.nvfp4_group_wgrad(dy, x, m, dw)
+    for g in (0, 17, 39):
+        o, r = sum(m[:g]), m[g]
+        one = [abi.matrix(q["data"][n * o // 2:n * (o + r) // 2].clone(), q["scale"][n * o // 16:n * (o + r) // 16].clone(),
+                          q["s2"][g * n:(g + 1) * n].clone()) for q, n in ((dy, N), (x, K))]
+        alone = torch.empty(1, N, K, device="cuda")
+        abi.nvfp4_group_wgrad(*one, [r], alone)
+        assert torch.equal(alone[0], dw[g])
