@@ -516,9 +516,12 @@ NVFP4RS_API size_t nvfp4_adapter_workspace_bytes(int64_t rows, int32_t rank);
  *   term where ids[t] == -1
  * X, W the NVFP4 operands [rows, K] and [N, K] (x_bf16's rowwise cast and the
  * shared weights), x, A, B bf16. u = factor (x A^T) is summed and kept in fp32. Its
- * product with B, whose factors keep u to 2^-25, is summed in fp32 and added in
- * fp32 to the projection before the one rounding of y. Infinities and NaN in A, B,
- * factor and u give what the formula gives, in the tokens that use them and no others.
+ * product with B takes bf16 terms of u whose sum is within 2^-25 of it for an
+ * fp32 y and within 2^-17 for a bf16 y (whose own rounding is 2^-8: the difference
+ * shows only where the adapter cancels the projection); it is summed in fp32 and added
+ * in fp32 to the projection before the one rounding of y. Infinities and NaN in A,
+ * B, factor and u give what the formula gives, in the tokens that use them and no
+ * others.
  *   x_bf16   device bf16 [rows, K]
  *   a_bf16   device bf16 [num_adapters, rank, K]
  *   b_bf16   device bf16 [num_adapters, N, rank]

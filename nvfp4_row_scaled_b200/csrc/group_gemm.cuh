@@ -547,9 +547,8 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t (&p)[3]) {
 // The adapters' share of a warp's 32 features x 32 rows (features n0 .., rows
 // row .. row + nc - 1): sum_r u[row][r] b[id][n][r], on the bf16 tensor cores, 16
 // features x 8 rows x 16 ranks an instruction. u is fp32: three bf16 terms of it
-// (2^-25 of u) multiply b and meet in the fp32 accumulator, for a bf16 result too (two
-// terms, 2^-17, show where the adapter cancels the projection; 8192 x 7168 x 2048, rank
-// 32: 159.5 us with two, 160.5 with three). Each distinct adapter
+// (2^-25 of u) multiply b and meet in the fp32 accumulator; a bf16 result, whose
+// own rounding is 2^-8, takes two (2^-17). Each distinct adapter
 // of the rows is one pass over the 8-row blocks that use it, with the other
 // rows' u as zeros -- which add nothing while b is finite, so a row's result does not
 // depend on its neighbours; the next pass's b is loaded meanwhile. A pass whose b
@@ -655,6 +654,7 @@ __device__ __forceinline__ void sum_adapters(float (&acc)[2][4][4], uint32_t& sl
         split3(u1.z, u1.w, p[3]);
 #pragma unroll
         for (int i = 2; i >= 0; i--) {
+          if (i == 2 && !a.out_f32) continue;
 #pragma unroll
           for (int m = 0; m < 2; m++) {
             mma_bf16(acc[m][j], w[m][0].x, w[m][1].x, w[m][0].y, w[m][1].y, p[0][i], p[1][i]);

@@ -280,9 +280,9 @@ def test_token_does_not_depend_on_the_size_of_the_call(K):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_precision_where_the_adapter_cancels_the_projection(dtype):
     """b = -p / u rounded to bf16, so that y is what that rounding leaves, 2^-9 of p or less. u is one product, f a x:
-    a and x of 8 bits, f of 24, rounded once (2^-24). Three bf16 terms of u are within 2^-25 of it.
-    Their products with b are exact, their sum is cut to 24 bits at most four times (2^-23 each), and
-    one addition to p follows."""
+    a and x of 8 bits, f of 24, rounded once (2^-24). For a bf16 y two bf16 terms of u are taken,
+    within 2^-17 of it, for an fp32 y three, within 2^-25. Their products with b are exact, their sum is cut
+    to 24 bits at most four times (2^-23 each), and one addition to p follows."""
     rows, K, N, R = 24, 64, 96, 8
     c = case(rows, K, N, R, rows, list(range(rows)), 13)
     c["xb"][:, 1:] = 0
@@ -296,8 +296,9 @@ def test_precision_where_the_adapter_cancels_the_projection(dtype):
     c["b"].zero_()
     c["b"][:, :, 0] = b.cuda()
     d = b.double() * u[:, None]
+    terms = 2.0 ** -17 if dtype == torch.bfloat16 else 2.0 ** -25
     y, st = run(c, dtype)
     assert st == 0
     want = p + d
     assert float(want.abs().max()) < 2.0 ** -8 * float(p.abs().max())
-    check(y, want, lim + (2.0 ** -25 + 2.0 ** -24 + 4 * 2.0 ** -23) * d.abs() + 2.0 ** -24 * want.abs())
+    check(y, want, lim + (terms + 2.0 ** -24 + 4 * 2.0 ** -23) * d.abs() + 2.0 ** -24 * want.abs())
