@@ -20,9 +20,9 @@
 // its adapters and keeps the rows that use them. A decode step (a different
 // adapter on every row) runs its adapters side by side; a prompt has one
 // adapter in most blocks and leaves the other slots empty.
-// Measured: 8192 rows x 7168 at rank 32 in 53 us (x at 2.2 TB/s, bound by the
-// latency of the row-wise loads; 1 to 3 CTAs a SM and 2 to 8 steps unrolled are alike),
-// 64 rows x 4096 with an adapter each at rank 16 in 8 us.
+// Measured: 8192 rows x 7168 at rank 32 in 54 us (x at 2.2 TB/s: 512 CTAs keep the SMs
+// busy for 64% of it, and their warps wait for the row-wise loads; 1 to 3 CTAs a SM and 2 to 8
+// steps unrolled are alike), 64 rows x 4096 with an adapter each at rank 16 in 8.5 us.
 #pragma once
 
 #include <cooperative_groups.h>

@@ -32,10 +32,12 @@
 // x `jt` J rows of one group, I tiles innermost so that concurrent CTAs share
 // the token tile and the group's weights in L2). Large problems run it on pairs
 // of CTAs (kPair): 256 I rows, 128 to a CTA, x up to 256 J rows of which each CTA
-// loads half, in one MMA over both SMs' tensor cores. What bounds a large product
-// is the 64 bytes a cycle at which an SM reads L2: a 256-element k block of
-// a 128 x 256 tile is 512 cycles of MMA and 54 KB (864 cycles) to one CTA, 38 KB
-// (608) to each of a pair. Five roles, joined by mbarriers:
+// loads half, in one MMA over both SMs' tensor cores. Why pairs: an SM reads 64 bytes
+// a cycle from L2, and a 256-element k block of a 128 x 256 tile is 512 cycles of MMA and
+// 54 KB (864 cycles) to one CTA, 38 KB (608) to each of a pair (gated: 46 KB, 736). A block
+// takes about 790 cycles at 8192 x 8192 x 8192 and 829 in a gated call of 80768 rows x 7168, under the
+// power cap's 1.40 and 1.14 GHz; at K = 2048, where a tile has 8 blocks and its stores take as
+// long, 970 to 1360. Five roles, joined by mbarriers:
 //   warp 0      data of each 256-element k block by TMA (128-byte swizzle) and
 //               tiled block scales by bulk copies
 //   warp 1      tensor memory, scale copies shared -> tensor memory, MMAs (in
@@ -53,9 +55,9 @@
 // MMAs start once the shared columns of this one have been read, which the
 // epilogue does first.
 //
-// Measured: 8192 x 8192 x 8192 in 213 us (5.1 PFLOP/s at the 1.5 GHz that the power cap
-// leaves), 269 with row-major scales; 128 experts of a few tokens at 4.7 TB/s of
-// weights; fp32 weight gradients stored at 5.3 TB/s.
+// Measured (30 calls in a row): 8192 x 8192 x 8192 in 216 us (5.1 PFLOP/s; in a loop of seconds 249
+// us, 4.4), 288 with row-major scales; 128 experts of a few tokens in 58 us, 4.8 TB/s of
+// all bytes; 16 fp32 weight gradients of 2048 x 4096 in 107 us, 5.0 TB/s of stores.
 //
 // Every wait is bounded. After a give-up the roles leave their loops, wait
 // (bounded) for what is in flight, and the status is reported where the call
@@ -548,7 +550,8 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t (&p)[3]) {
 // row .. row + nc - 1): sum_r u[row][r] b[id][n][r], on the bf16 tensor cores, 16
 // features x 8 rows x 16 ranks an instruction. u is fp32: three bf16 terms of it
 // (2^-25 of u) multiply b and meet in the fp32 accumulator; a bf16 result, whose
-// own rounding is 2^-8, takes two (2^-17). Each distinct adapter
+// own rounding is 2^-8, takes two (2^-17; a third costs a decode step of 64 adapters 2 of 22.6 us).
+// Each distinct adapter
 // of the rows is one pass over the 8-row blocks that use it, with the other
 // rows' u as zeros -- which add nothing while b is finite, so a row's result does not
 // depend on its neighbours; the next pass's b is loaded meanwhile. A pass whose b
@@ -559,7 +562,7 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t (&p)[3]) {
 // the projection, so a tile's first chunk is summed while the tile is still being
 // multiplied. What bounds it: these instructions wait behind the projection's
 // tcgen05 ones, about 100 cycles each, so the fewer the better. In fp32 FMAs, with
-// u read from shared memory, 8192 rows at rank 32 took 191 us against 142.
+// u read from shared memory, 8192 rows at rank 32 took 191 us against 147.
 // acc[m][j][e]: feature 16 m + 8 (e / 2) + lane / 4, row 8 j + 2 (lane % 4) + e % 2.
 __device__ __forceinline__ void sum_adapters(float (&acc)[2][4][4], uint32_t& slow, const GemmArgs& a, int64_t row,
                                              int64_t n0, int features, int nc, int lane) {

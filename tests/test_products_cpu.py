@@ -151,3 +151,45 @@ def test_splits_whose_sum_overflows(L, m):
     assert L.nvfp4_group_amax(FAKE, 64, 128, ap, n, FAKE, FAKE, None) == BAD
     assert L.nvfp4_group_cast(FAKE, 64, 128, ap, n, FAKE, FAKE, ctypes.byref(out), None) == BAD
     assert L.nvfp4_mx_group_cast(FAKE, 64, 128, ap, n, ctypes.byref(mx), None) == BAD
+
+
+def test_calls_run_on_the_tensors_device(monkeypatch):
+    """Tensors on a device that is not the current one: the call is made with that device current, on its
+    current stream, and the former device is current again; a stream of another device is refused."""
+    state, seen = {"current": 0}, []
+
+    class Guard:
+        def __init__(self, dev):
+            self.dev = torch.device(dev).index
+
+        def __enter__(self):
+            self.before, state["current"] = state["current"], self.dev
+
+        def __exit__(self, *exc):
+            state["current"] = self.before
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 1000 + index, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: state["current"], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+
+    def entry(*args):
+        seen.append((state["current"], args))
+        return OK
+    one = torch.device("cuda:1")
+    abi._run(one, None, "call", entry, 7)
+    assert seen == [(1, (7, 1001))] and state["current"] == 0
+
+    class Stream:
+        cuda_stream = 55
+
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+    abi._run(one, Stream(1), "call", entry)
+    assert seen[-1] == (1, (55,)) and state["current"] == 0
+    with pytest.raises(ValueError, match="stream is on"):
+        abi._run(one, Stream(0), "call", entry)
+
+    def fails(*args):
+        return abi.NVFP4_ERR_UNSUPPORTED
+    with pytest.raises(abi.NVFP4Error):
+        abi._run(one, None, "call", fails)
+    assert state["current"] == 0 and len(seen) == 2
