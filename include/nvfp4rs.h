@@ -481,9 +481,10 @@ NVFP4RS_API nvfp4_status nvfp4_group_gated_gemm_graphsafe(const nvfp4_matrix* x,
  * saves them) and s = 1 / (1 + e^-g):
  *   d_gate_up[t][f]     = dh u s (1 + g (1 - s))
  *   d_gate_up[t][F + f] = dh g s
- * in fp32, rounded once to bf16 (hardware exponential and quotient: before it within
- * (12 + |g|) 2^-23 of itself, d_up, and of 2 |dh u s| (1 + |g|), d_gate; gates below -174 may give 0 where
- * dh, up and e^g together are below 2^-116). In the same pass the row amax and the
+ * in fp32, rounded once to bf16 (hardware exponential and quotient: before that
+ * rounding within (12 + |g|) 2^-23 of itself, d_up, and of 2 |dh u s| (1 + |g|),
+ * d_gate; where e^(g/2), or it times dh or u, is below 2^-126 the result may
+ * be 0). In the same pass the row amax and the
  * per-group column amax of d_gate_up, bit-identical to nvfp4_group_amax of it:
  * the scale sources of its nvfp4_group_cast, after which nvfp4_group_gemm (on
  * the weights' colwise cast) and nvfp4_group_wgrad finish the backward pass.

@@ -3,8 +3,8 @@
 // For h = silu(g) u with the saved pre-activations (g, u) = gate_up[t][f],
 // gate_up[t][F + f] and the incoming dh:
 //   d_gate = dh u s (1 + g (1 - s)),   d_up = dh g s,   s = 1 / (1 + e^-g)
-// in fp32 (gated_grad below has the form that keeps its range), rounded once to bf16 into d_gate_up [rows][2F]. That buffer is cast
-// to NVFP4 next (both directions: the input gradient reads the rows, the
+// in fp32 (gated_grad below has the form that keeps its range), rounded once to
+// bf16 into d_gate_up [rows][2F]. That buffer is cast to NVFP4 next (both directions: the input gradient reads the rows, the
 // weight gradient the columns), so the same pass also yields what the grouped
 // amax of it would (TransformerEngine #3649, Description): the row amax and the
 // per-group column amax of the ROUNDED values, bit for bit, which saves that
@@ -62,7 +62,8 @@ __device__ __forceinline__ void st_stream(uint4* p, uint4 v) {
 
 // One element: (d_gate, d_up). With h = e^(-|g|/2), m = 1 for g >= 0 and h below, r = 1 / (1 + h^2):
 // s = m^2 r and 1 - s = (g >= 0 ? h^2 : 1) r, with no cancellation, no divisor above 2 and
-// no s below 2^-126 on its own: dh and u take a factor m each.
+// no s below 2^-126 on its own: dh and u take a factor m each (either way round some products of
+// huge and tiny factors leave fp32's range; here those with |dh| m or |u| m below 2^-126).
 __device__ __forceinline__ float2 gated_grad(float dh, float g, float u) {
   const float h = half_exp(g), q = h * h, r = fast_rcp(1.0f + q);
   const bool pos = g >= 0.0f;

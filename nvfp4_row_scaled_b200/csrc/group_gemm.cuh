@@ -550,15 +550,15 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t (&p)[3]) {
 // row .. row + nc - 1): sum_r u[row][r] b[id][n][r], on the bf16 tensor cores, 16
 // features x 8 rows x 16 ranks an instruction. u is fp32: three bf16 terms of it
 // (2^-25 of u) multiply b and meet in the fp32 accumulator; a bf16 result, whose
-// own rounding is 2^-8, takes two (2^-17; a third costs a decode step of 64 adapters 2 of 22.6 us).
-// Each distinct adapter
-// of the rows is one pass over the 8-row blocks that use it, with the other
-// rows' u as zeros -- which add nothing while b is finite, so a row's result does not
-// depend on its neighbours; the next pass's b is loaded meanwhile. A pass whose b
-// (these features, these ranks) holds an infinity or NaN, which 0 would not cancel,
-// is left out, and so is a row whose u holds an infinity or a value that bf16 rounds to
-// one (split3 would give inf - inf; a NaN stays one): `slow` returns those rows, their sums zero, for add_slow(). The ranks are numbered as a
-// lane loads them (8 of a row, 16 bytes), alike on both sides. Reads nothing of
+// own rounding is 2^-8, takes two (2^-17; a third takes a decode step of 64 adapters
+// from 22.6 to 24.6 us). Each distinct adapter of the rows is one pass over the 8-row
+// blocks that use it, with the other rows' u as zeros -- which add nothing while b is
+// finite, so a row's result does not depend on its neighbours; the next pass's b is
+// loaded meanwhile. A pass whose b (these features, these ranks) holds an infinity or
+// NaN, which 0 would not cancel, is left out, and so is a row whose u holds an infinity
+// or a value that bf16 rounds to one (split3 would give inf - inf; a NaN stays one):
+// `slow` returns those rows, their sums zero, for add_slow(). The ranks are numbered as
+// a lane loads them (8 of a row, 16 bytes), alike on both sides. Reads nothing of
 // the projection, so a tile's first chunk is summed while the tile is still being
 // multiplied. What bounds it: these instructions wait behind the projection's
 // tcgen05 ones, about 100 cycles each, so the fewer the better. In fp32 FMAs, with

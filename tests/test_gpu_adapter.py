@@ -302,3 +302,13 @@ def test_precision_where_the_adapter_cancels_the_projection(dtype):
     want = p + d
     assert float(want.abs().max()) < 2.0 ** -8 * float(p.abs().max())
     check(y, want, lim + (terms + 2.0 ** -24 + 4 * 2.0 ** -23) * d.abs() + 2.0 ** -24 * want.abs())
+
+
+@pytest.mark.parametrize("rows,K", [(1, 16), (3, 48), (129, 16), (7, 1008), (131, 176)])
+def test_scales_that_end_inside_a_word(rows, K):
+    """The projection's row-major scales end 1, 2 or 3 bytes into an aligned word (rows K / 16 bytes)."""
+    assert rows * (K // 16) % 4
+    c = case(rows, K, 48, 8, 3, spread(rows, 3, "mixed"), rows + K)
+    y, st = run(c, torch.float32)
+    assert st == 0
+    check(y, *reference(c))

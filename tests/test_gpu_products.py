@@ -397,6 +397,10 @@ def test_scales_that_end_inside_a_word(m, K):
     y = torch.empty(rows, 2 * N, device="cuda")
     abi.nvfp4_group_gemm(x, m, w, y)
     check(y, want, lim)
+    fd, offs, st = routings(m, K, rows)
+    z = torch.empty_like(y)
+    abi.nvfp4_group_gemm_graphsafe(x, fd, offs, w, z, st)
+    assert int(st.item()) == 0 and torch.equal(y, z)
     x["s2"] *= 2.0 ** -8
     h, p = torch.empty(rows, N, dtype=torch.bfloat16, device="cuda"), torch.empty(rows, 2 * N, dtype=torch.bfloat16, device="cuda")
     abi.nvfp4_group_gated_gemm(x, m, w, h, gate_up=p)
