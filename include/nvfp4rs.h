@@ -369,7 +369,8 @@ NVFP4RS_API nvfp4_status nvfp4_mx_dequantize(const uint8_t* data, const uint8_t*
  * backward of the grouped linear layer), on the block-scaled tensor cores.
  *
  * One operand: a row-major matrix in NVFP4 with one fp32 factor a row, as a
- * cast writes it. Its value is (e2m1(code) * e4m3(scale)) * s2[row].
+ * cast writes it. Its value is (e2m1(code) * e4m3(scale)) * s2[row]; scale bytes
+ * are 0x00 to 0x7F (no sign, as a cast writes them).
  *   - rowwise outputs of a cast: row_data / row_scale / row_s2, [rows, K];
  *   - colwise outputs: col_data / col_scale / col_s2, per group [K, m_g] at
  *     byte K*o_g/2 (codes), K*o_g/16 (scales) and entry g*K (factors).

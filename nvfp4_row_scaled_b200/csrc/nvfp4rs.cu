@@ -879,7 +879,8 @@ template <int kMT, int kNT>
 nvfp4_status launch_shrink(const ShrinkArgs& s, int sms, cudaStream_t stream) {
   constexpr int kTok = 16 * kMT;
   const int64_t blocks = (s.rows + kTok - 1) / kTok;
-  // adapters side by side while that fills the GPU
+  // adapters side by side while that fills the GPU: 64 rows of 4096 with 64 adapters 22 us a call, one after
+  // the other 68; 512 rows with 8: 28.6 and 28.7
   int slots = 1;
   while (slots < kTok && slots < s.adapters && blocks * slots < sms) slots *= 2;
   // K over a pair of CTAs where each of their 16 warps gets a step of 32. By K alone: the order
@@ -1311,7 +1312,9 @@ nvfp4_status nvfp4_adapter_gemm(const void* x_bf16, const nvfp4_matrix* x, int64
                   .set(stream));
   const ShrinkArgs sh{static_cast<const uint16_t*>(x_bf16), static_cast<const uint16_t*>(a_bf16), factor, ids_dev, u,
                       status_dev, static_cast<int32_t>(rows), static_cast<int32_t>(K), num_adapters};
-  // 32-row blocks halve the reads of A once there are blocks for every SM
+  // 32-row blocks halve the reads of A once there are blocks for every SM: 8192 rows of 7168 at rank 32 163 us a
+  // call with 16 rows, 158 with 32 (rank 64: 214 and 226; an adapter of its own every 2 rows: 243
+  // and 290); 64 rows of 7168 at rank 64: 25 and 35
   s = rows >= 32 * static_cast<int64_t>(sms) ? launch_shrink_rank<2>(sh, rank, sms, stream)
                                              : launch_shrink_rank<1>(sh, rank, sms, stream);
   if (s != NVFP4_OK) return s;
