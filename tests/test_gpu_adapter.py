@@ -1,4 +1,6 @@
 """Low-rank adapters beside a shared NVFP4 projection against fp64."""
+import os
+
 import pytest
 import torch
 
@@ -312,3 +314,22 @@ def test_scales_that_end_inside_a_word(rows, K):
     y, st = run(c, torch.float32)
     assert st == 0
     check(y, *reference(c))
+
+
+def test_two_streams_at_once():
+    """Decode steps and prompts on two streams, a workspace each: the bits of one call after the other."""
+    if os.environ.get("NVFP4RS_LIBRARY", "").endswith("_debug.so"):
+        pytest.skip("the bounds-checked build keeps one table of ranges: one call at a time")
+    cs = [case(64, 1024, 512, 16, 64, spread(64, 64, "each"), 15), case(3000, 1024, 512, 32, 5, spread(3000, 5, "runs"), 16)]
+    want = [run(c)[0].clone() for c in cs]
+    ys = [torch.empty_like(w) for w in want]
+    ws = [abi.alloc_adapter_workspace(c["xb"].shape[0], c["a"].shape[1]) for c in cs]
+    st = [torch.zeros(1, dtype=torch.int32, device="cuda") for _ in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for c, y, w, s, stream in zip(cs, ys, ws, st, streams):
+            abi.nvfp4_adapter_gemm(c["xb"], c["x"], c["w"], c["a"], c["b"], c["f"], c["ids"], y, w, s, stream=stream)
+    torch.cuda.synchronize()
+    for y, w, s in zip(ys, want, st):
+        assert int(s.item()) == 0 and torch.equal(y, w)
